@@ -1,7 +1,7 @@
 /*
  * ssm.h -- C ABI of libssm.so, a B200 (sm_100a) selective-scan library.
  *
- * Three operations:
+ * Three scans, the gated delta rule and the norms around a block:
  *
  *  ssm_scan_fwd    Mamba S6 selective scan, one direction.
  *                  Defined by the discrete recurrence of the Mamba2 page
@@ -25,6 +25,15 @@
  *                  with A a scalar per head, computed chunk by chunk -- matrix
  *                  products (tensor cores) inside each chunk and the chunk state
  *                  passed on between chunks.
+ *
+ *  gdr_chunk_fwd, gdr_chunk_bwd, gdr_step
+ *                  the gated delta rule: SSD's decaying matrix state, written
+ *                  by the error of what it returns for the key -- sequences,
+ *                  their gradients, one decode step.
+ *
+ *  gated_norm_*, residual_norm_*
+ *                  the norm of a block's mixed output with its gate, and the
+ *                  residual update with the next block's norm, with gradients.
  *
  * Conventions shared by all entry points
  *  - Every tensor argument is a DEVICE pointer to a contiguous row-major array
@@ -460,6 +469,192 @@ SSM_API ssm_status ssd_chunk_fwd(const ssd_dims *dims, const void *x, const void
                          const void *B, const void *C, const float *D, const void *z,
                          void *out, float *last_state, void *workspace,
                          size_t workspace_bytes, void *stream);
+
+/* Gated delta rule problem size.  Supported: headdim_k and headdim_v each 64
+ * or 128; nheads_v a multiple of nheads_k (value head h reads query / key
+ * head h / (nheads_v / nheads_k)); dtype SSM_BF16 for the chunked entry
+ * points, SSM_F32 or SSM_BF16 for gdr_step. */
+typedef struct {
+    int64_t batch;      /* B  */
+    int64_t seqlen;     /* L  */
+    int64_t nheads_k;   /* Hk */
+    int64_t nheads_v;   /* Hv */
+    int64_t headdim_k;  /* K  */
+    int64_t headdim_v;  /* V  */
+    int32_t dtype;
+} gdr_dims;
+
+/* Inputs of the gated delta rule. */
+typedef struct {
+    const void *q, *k;        /* (B, L, Hk, K) dtype, required                          */
+    const void *v;            /* (B, L, Hv, V) dtype, required                          */
+    const void *delta;        /* (B, L, Hv) dtype, required: raw time step              */
+    const float *delta_bias;  /* (Hv) float32, or NULL for no bias                      */
+    const float *A;           /* (Hv) float32, required; the log decay of a step is dt A */
+    const void *beta;         /* (B, L, Hv) dtype, required: writing strength           */
+    float scale;              /* factor of q (usually K^-1/2)                           */
+    int32_t delta_softplus;   /* 1: dt = softplus(delta + delta_bias), 0: their sum     */
+    int32_t beta_sigmoid;     /* 1: b = sigmoid(beta), 0: b = beta                      */
+    int32_t qk_l2norm;        /* 1: q and k are divided by sqrt(sum of squares + 1e-6)  */
+} gdr_inputs;
+
+/* Bytes of device workspace gdr_chunk_fwd needs for `dims` (0 if none or if
+ * dims are not supported). */
+SSM_API size_t gdr_chunk_workspace_size(const gdr_dims *dims);
+
+/*
+ * Gated delta rule over sequences.  Like ssd_chunk_fwd a recurrence with a
+ * matrix state per head and a scalar decay exp(dt A), but each step first
+ * takes away what the state already returns for the key (the delta rule), so
+ * a key that comes again overwrites instead of adding.  Per value head, from
+ * S = initial_state (zero if NULL), for every t:
+ *     a = exp(dt A);  S = a S
+ *     S = S + b (v - S k) k^T;   out = S (scale q)
+ * with dt, b and the norms of q and k as gdr_inputs describes.  Computed in
+ * chunks of 64 steps (matrix products inside a chunk, the state handed from
+ * chunk to chunk in float32) or, for short sequences, step by step.
+ *   out           (B, L, Hv, V) dtype, written
+ *   initial_state (B, Hv, V, K) float32 or NULL; may be the same buffer as
+ *                 last_state (updated in place)
+ *   last_state    (B, Hv, V, K) float32 or NULL: the state after the last step
+ * A padded position with dt = 0 and b = 0 (and
+ * finite q, k, v) leaves the state as it is.  An empty call (B, L, Hk or Hv
+ * zero) launches no kernel and copies initial_state (or zeros) to last_state.
+ */
+SSM_API ssm_status gdr_chunk_fwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state,
+                                 void *out, float *last_state, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/*
+ * One step of the gated delta rule from a stored state (decoding):
+ * dims->seqlen must be 1; q, k (B, Hk, K), v (B, Hv, V), delta and beta
+ * (B, Hv); state (B, Hv, V, K) float32 read and written in place; out
+ * (B, Hv, V) dtype written.  No workspace.
+ */
+SSM_API ssm_status gdr_step(const gdr_dims *dims, const gdr_inputs *in, float *state, void *out, void *stream);
+
+/* Gradients of gdr_chunk_fwd.  Those of tensors in the call's dtype have
+ * that dtype (summed in float32, rounded once). */
+typedef struct {
+    void *dq, *dk;          /* (B, L, Hk, K) dtype, required: summed over a key head's value heads */
+    void *dv;               /* (B, L, Hv, V) dtype, required        */
+    void *ddelta;           /* (B, L, Hv) dtype, required: of the raw delta */
+    void *dbeta;            /* (B, L, Hv) dtype, required: of the raw beta  */
+    float *dA;              /* (Hv) float32, required               */
+    float *ddelta_bias;     /* (Hv) float32: required when delta_bias is given */
+    float *dinitial_state;  /* (B, Hv, V, K) float32, or NULL       */
+} gdr_grads;
+
+/* Bytes of device workspace gdr_chunk_bwd needs for `dims` (0 if dims are
+ * not supported). */
+SSM_API size_t gdr_chunk_bwd_workspace_size(const gdr_dims *dims);
+
+/*
+ * Gradients of gdr_chunk_fwd for incoming gradients of out (dout, (B, L, Hv,
+ * V) dtype, required) and of last_state (dlast_state, (B, Hv, V, K) float32
+ * or NULL).  The states are recomputed, so nothing from the forward call is
+ * needed.  Every gradient is written, not accumulated, and sums in a fixed
+ * order: the same call gives the same bits.
+ */
+SSM_API ssm_status gdr_chunk_bwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state,
+                                 const void *dout, const float *dlast_state, const gdr_grads *grads,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Norms around a block (sizes shared by both kinds below).  dim and group
+ * must be multiples of 4 for SSM_F32 and of 8 for SSM_BF16
+ * (SSM_ERR_MISALIGNED) and group at most 8192 (SSM_ERR_UNSUPPORTED_SHAPE);
+ * every sum is float32.
+ */
+typedef struct {
+    int64_t rows;    /* positions: usually B L, or B L H for norms of heads */
+    int64_t dim;     /* channels of a row */
+    int64_t group;   /* channels normed together; divides dim */
+    float eps;       /* added to the mean square, >= 0 */
+    int32_t dtype;
+} norm_dims;
+
+/*
+ * RMS norm of a block's mixed output with its SiLU gate (the norm between
+ * the scan and the output projection of a Mamba2 or delta-rule block), per
+ * group of channels u of a row:
+ *   n(u) = u / sqrt(mean(u^2) + eps)
+ *   out  = n(x silu(z)) w          norm_before_gate = 0
+ *   out  = n(x) w silu(z)          norm_before_gate = 1
+ *   x, z, out (rows, dim) dtype (z may be NULL: no gate);  weight (dim) float32
+ * out may be the same buffer as x or z.
+ */
+SSM_API ssm_status gated_norm_fwd(const norm_dims *dims, const void *x, const void *z, const float *weight,
+                                  int norm_before_gate, void *out, void *stream);
+
+/* Bytes of device workspace gated_norm_bwd needs for `dims`. */
+SSM_API size_t gated_norm_bwd_workspace_size(const norm_dims *dims);
+
+/* Gradients of gated_norm_fwd for dout (rows, dim) dtype: dx, dz (rows, dim)
+ * dtype (dz required when z is given) and dweight (dim) float32, summed over
+ * the rows in a fixed order. */
+SSM_API ssm_status gated_norm_bwd(const norm_dims *dims, const void *x, const void *z, const float *weight,
+                                  int norm_before_gate, const void *dout, void *dx, void *dz, float *dweight,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The residual stream between two blocks: the block's output x joins it,
+ * optionally normed and scaled first, and the next block's input is its norm
+ * (one pass; the Vim block's Add + Norm).  group must equal dim.
+ *   t            = x, or x / sqrt(mean(x^2) + eps) post_weight
+ *   residual_out = alpha residual + scale t      (rounded to its type)
+ *   out          = n(residual_out) weight + bias
+ * n is the RMS norm, or with layer_norm = 1 the layer norm
+ * (r - mean) / sqrt(var + eps).
+ *   x, out        (rows, dim) dtype
+ *   residual      (rows, dim) or NULL (the first block: residual_out = scale t)
+ *   residual_out  (rows, dim); both float32 where residual_f32 is set, else dtype.
+ *                 May be the same buffer as residual
+ *   weight (dim), bias (dim) or NULL, post_weight (dim) or NULL: float32
+ *   scale  (samples, dim) float32 or NULL: samples = 1 is a layer scale;
+ *          samples = B a gate per sample; row r reads scale[r / (rows / samples)]
+ */
+typedef struct {
+    const float *weight;       /* required */
+    const float *bias;
+    const float *scale;
+    const float *post_weight;
+    int64_t samples;           /* >= 1, divides rows */
+    float alpha;
+    int32_t layer_norm;
+    int32_t residual_f32;      /* ignored for SSM_F32, whose stream is float32 */
+} residual_norm_params;
+
+SSM_API ssm_status residual_norm_fwd(const norm_dims *dims, const residual_norm_params *p, const void *x,
+                                     const void *residual, void *residual_out, void *out, void *stream);
+
+/* Gradients of residual_norm_fwd: float32 ones are required where their
+ * input is given, and summed over the rows in a fixed order. */
+typedef struct {
+    void *dx;             /* (rows, dim) dtype, required */
+    void *dresidual;      /* (rows, dim) in the stream's type, or NULL (no residual) */
+    float *dweight;       /* (dim), required */
+    float *dbias;         /* (dim) */
+    float *dscale;        /* (samples, dim) */
+    float *dpost_weight;  /* (dim) */
+} residual_norm_grads;
+
+/* Bytes of device workspace residual_norm_bwd needs (0 for invalid arguments). */
+SSM_API size_t residual_norm_bwd_workspace_size(const norm_dims *dims, const residual_norm_params *p);
+
+/*
+ *   residual_out   what the forward call wrote
+ *   dout           (rows, dim) dtype: gradient of out
+ *   dresidual_out  (rows, dim) in the stream's type, or NULL (zero): gradient
+ *                  of residual_out from its later uses.  May be the same
+ *                  buffer as dresidual
+ *   x              the forward call's x; may be NULL where neither scale nor
+ *                  post_weight is given
+ */
+SSM_API ssm_status residual_norm_bwd(const norm_dims *dims, const residual_norm_params *p, const void *x,
+                                     const void *residual_out, const void *dout, const void *dresidual_out,
+                                     const residual_norm_grads *grads, void *workspace,
+                                     size_t workspace_bytes, void *stream);
 
 /*
  * Waits for `stream`, then reports (and clears) the library's device-side

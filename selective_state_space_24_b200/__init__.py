@@ -23,6 +23,10 @@ Entry points (names as in include/ssm.h):
   the conv computed inside the scan
 * ``bidir_scan_fwd(x, delta, fwd, bwd, ...)``  Vision-Mamba bidirectional scan
 * ``ssd_chunk_fwd(x, delta, A, B, C, ...)``  Mamba2 SSD chunked scan
+* ``gdr_chunk_fwd`` / ``gdr_chunk_bwd`` / ``gdr_step``  the gated delta rule:
+  sequences, their gradients, one decode step (block_ops.py, as the next two)
+* ``gated_norm_fwd`` / ``gated_norm_bwd``  RMS norm with a SiLU gate
+* ``residual_norm_fwd`` / ``residual_norm_bwd``  residual update and next norm
 
 Each also exists in raw form in ``capi`` (ctypes functions taking plain
 integers for pointers), which the tests use to check the boundary itself.
@@ -694,3 +698,9 @@ def scan_plan(batch, seqlen, dim, dstate, dtype=SSM_F32, bidirectional=False):
 def check_device(stream=None):
     """Synchronise and raise if a kernel reported a device-side timeout."""
     _check(capi().ssm_check_device(_stream_handle(stream)), "ssm_check_device")
+
+
+from .block_ops import *   # noqa: E402,F401,F403  (needs the names above)
+from . import block_ops as _block_ops   # noqa: E402
+
+SIGNATURES.update(_block_ops.SIGNATURES)

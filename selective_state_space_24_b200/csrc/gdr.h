@@ -1,0 +1,41 @@
+// gdr.h -- launcher interface of the gated delta rule kernels.  Not part of
+// the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace ssm {
+
+struct GdrArgs {
+    int Bsz, L, Hk, Hv, K, V;
+    int dtype;                       // 0 = float32, 1 = bf16
+    int softplus, sigmoid, l2norm;
+    float scale;
+    const void *q, *k, *v, *delta, *beta;
+    const float *bias, *A;
+    const float *init;               // (B, Hv, V, K) or nullptr
+    void *out;
+    float *last;                     // (B, Hv, V, K) or nullptr
+    void *workspace;
+};
+
+// Step by step, the state in registers: one token (gdr_step) or short
+// sequences.
+cudaError_t launch_gdr_recurrent(const GdrArgs &a, cudaStream_t st);
+
+size_t gdr_chunk_ws_bytes(const GdrArgs &a);
+cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st);
+
+struct GdrBwdArgs {
+    GdrArgs f;
+    const void *dout;
+    const float *dlast;              // or nullptr
+    void *dq, *dk, *dv, *ddelta, *dbeta;
+    float *dA, *dbias, *dinit;       // dbias, dinit may be nullptr
+};
+size_t gdr_bwd_ws_bytes(const GdrArgs &a);
+cudaError_t launch_gdr_bwd(const GdrBwdArgs &a, cudaStream_t st);
+
+}  // namespace ssm

@@ -1,0 +1,421 @@
+// residual_norm.cu -- the residual stream between two blocks and the next
+// block's norm, and its gradients.  Per row:
+//     t = x, or x p post with p = (mean x^2 + eps)^-1/2
+//     r = alpha residual + scale t   (rounded to the stream's type)
+//     out = n(r) weight + bias,   n(r) = (r - m) k,  k = (mean (r - m)^2 + eps)^-1/2
+// with m = mean(r) for the layer norm, 0 for the RMS norm.  Backward, from
+// g = dout weight and y = n(r):
+//     dr = dres_out + k (g - y mean(g y) [- mean(g)]),  dresidual = alpha dr
+//     dscale = sum dr t,  dt = dr scale
+//     dpost = sum dt x p, e = dt post,  dx = p (e - x p mean(e x p))   (dx = dt without post)
+//     dweight = sum dout y, dbias = sum dout
+//
+// Bound by HBM: one pass, a row stays in registers through up to three
+// dependent sums (the mean is taken before the squares, which keeps the
+// variance exact for rows far from zero).  Thread layout and column sums as
+// in gated_norm.cu; with a scale per sample a block's rows are of one sample.
+#include <type_traits>
+
+#include "norm_common.cuh"
+
+namespace ssm {
+namespace {
+
+NormPlan residual_plan(int64_t rows, int64_t sets, int dim)
+{
+    NormPlan p = norm_threads(dim);
+    const int64_t need = (rows / sets + p.rows_at_once - 1) / p.rows_at_once;
+    const int64_t most = ((int64_t)148 * (2048 / p.threads) + sets - 1) / sets;
+    p.parts = (int)(need < most ? need : most);
+    return p;
+}
+
+// The sets of rows that never share a block: the samples where a scale's
+// gradient is summed over each of them, else all rows are one.
+int64_t row_sets(int64_t samples, bool has_scale) { return has_scale ? samples : 1; }
+
+// a row's mean (LAYER) and (mean square + eps)^-1/2 from its registers; r is
+// centred in place.  The rounded mean of a row far from zero is off by up to
+// half a step of that mean; the centred values (exact differences) show by
+// how much, in the same sum that takes their squares.
+template <bool LAYER, int NV, int E>
+__device__ __forceinline__ float norm_stats(float (&r)[NV][E], const bool (&in)[NV], float inv, float eps, int tpr,
+                                            RedSmem &red, int &turn)
+{
+    float s[2] = {0.f, 0.f};
+    if (LAYER) {
+        float m[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                m[0] += r[v][e];   // zero outside the row
+        row_sum<1>(m, tpr, red, turn);
+        m[0] *= inv;
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                r[v][e] = in[v] ? r[v][e] - m[0] : 0.f;
+                s[1] += r[v][e];
+            }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; v++)
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            s[0] = fmaf(r[v][e], r[v][e], s[0]);
+    if (LAYER) {
+        row_sum<2>(s, tpr, red, turn);
+        const float off = s[1] * inv;
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                r[v][e] -= in[v] ? off : 0.f;
+        return rsqrtf(fmaf(-off, off, s[0] * inv) + eps);
+    }
+    float one[1] = {s[0]};
+    row_sum<1>(one, tpr, red, turn);
+    return rsqrtf(one[0] * inv + eps);
+}
+
+template <typename R> __device__ __forceinline__ float rounded(float v);
+template <> __device__ __forceinline__ float rounded<float>(float v) { return v; }
+template <> __device__ __forceinline__ float rounded<__nv_bfloat16>(float v)
+{
+    return __bfloat162float(__float2bfloat16_rn(v));
+}
+
+template <typename T, typename R, bool LAYER>
+__global__ void __launch_bounds__(512) residual_fwd_kernel(const ResidualArgs a, int tpr, int rpb)
+{
+    constexpr int E = Vec<T>::N, NV = kNormElems / E;
+    __shared__ RedSmem red;
+    const int lane_r = threadIdx.x % tpr, sub = threadIdx.x / tpr;
+    const int nv = a.dim / E;
+    const T *x = static_cast<const T *>(a.x);
+    const R *res = static_cast<const R *>(a.residual);
+    const float inv = 1.f / (float)a.dim;
+    const int64_t per = a.rows / a.samples;
+    int turn = 0;
+    bool in[NV];
+#pragma unroll
+    for (int v = 0; v < NV; v++)
+        in[v] = lane_r + v * tpr < nv;
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
+        const int64_t row = r0 + sub;
+        const bool live = row < a.rows;
+        float t[NV][E], rv[NV][E];
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int64_t at = row * a.dim + (lane_r + v * tpr) * E;
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                t[v][e] = rv[v][e] = 0.f;
+            if (live && in[v]) {
+                Vec<T>::load(x + at, t[v]);
+                if (res)
+                    load_row<R, E>(res + at, rv[v]);
+            }
+        }
+        if (a.post) {
+            float s[1] = {0.f};
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    s[0] = fmaf(t[v][e], t[v][e], s[0]);
+            row_sum<1>(s, tpr, red, turn);
+            const float p = rsqrtf(s[0] * inv + a.eps);
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+                if (in[v]) {
+                    float w[E];
+                    load_f32<E>(a.post + (lane_r + v * tpr) * E, w);
+#pragma unroll
+                    for (int e = 0; e < E; e++)
+                        t[v][e] *= p * w[e];
+                }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            if (a.scale && live && in[v]) {
+                float w[E];
+                load_f32<E>(a.scale + (a.samples == 1 ? 0 : row / per) * a.dim + (lane_r + v * tpr) * E, w);
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    t[v][e] *= w[e];
+            }
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                rv[v][e] = rounded<R>(res ? fmaf(a.alpha, rv[v][e], t[v][e]) : t[v][e]);
+            if (live && in[v])
+                store_row<R, E>(static_cast<R *>(a.res_out) + row * a.dim + (lane_r + v * tpr) * E, rv[v]);
+        }
+        const float k = norm_stats<LAYER>(rv, in, inv, a.eps, tpr, red, turn);
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (live && in[v]) {
+                const int c = (lane_r + v * tpr) * E;
+                float w[E], b[E], o[E];
+                load_f32<E>(a.weight + c, w);
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    b[e] = 0.f;
+                if (a.bias)
+                    load_f32<E>(a.bias + c, b);
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    o[e] = fmaf(rv[v][e] * k, w[e], b[e]);
+                Vec<T>::store(static_cast<T *>(a.out) + row * a.dim + c, o);
+            }
+    }
+}
+
+// A variant for each set of column sums (registers for the others are not kept).
+template <typename T, typename R, bool LAYER, bool BIAS, bool SCALE, bool POST>
+__global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a, int tpr, int rpb, int parts)
+{
+    constexpr int E = Vec<T>::N, NV = kNormElems / E;
+    __shared__ RedSmem red;
+    extern __shared__ float cols[];   // (dim)
+    const int lane_r = threadIdx.x % tpr, sub = threadIdx.x / tpr;
+    const int nv = a.dim / E;
+    const int64_t set = blockIdx.x / parts;
+    const int part = blockIdx.x % parts;
+    const int64_t per = SCALE ? a.rows / a.samples : a.rows;
+    const int64_t row_end = (set + 1) * per;
+    const float inv = 1.f / (float)a.dim;
+    int turn = 0;
+    bool in[NV];
+    float dw[NV][E], db[BIAS ? NV : 1][E], dsc[SCALE ? NV : 1][E], dpo[POST ? NV : 1][E];
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+        in[v] = lane_r + v * tpr < nv;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            dw[v][e] = 0.f;
+            if (BIAS)
+                db[v][e] = 0.f;
+            if (SCALE)
+                dsc[v][e] = 0.f;
+            if (POST)
+                dpo[v][e] = 0.f;
+        }
+    }
+    for (int64_t r0 = set * per + (int64_t)part * rpb; r0 < row_end; r0 += (int64_t)parts * rpb) {
+        const int64_t row = r0 + sub;
+        const bool live = row < row_end;
+        float y[NV][E], g[NV][E];   // the stream (then its norm), dout (then dr)
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int64_t at = row * a.dim + (lane_r + v * tpr) * E;
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                y[v][e] = g[v][e] = 0.f;
+            if (live && in[v]) {
+                load_row<R, E>(static_cast<const R *>(a.res_out) + at, y[v]);
+                Vec<T>::load(static_cast<const T *>(a.dout) + at, g[v]);
+            }
+        }
+        const float k = norm_stats<LAYER>(y, in, inv, a.eps, tpr, red, turn);
+        float s[2] = {0.f, 0.f};   // sums of g y and g
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (in[v]) {
+                float w[E];
+                load_f32<E>(a.weight + (lane_r + v * tpr) * E, w);
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    y[v][e] *= k;
+                    dw[v][e] = fmaf(g[v][e], y[v][e], dw[v][e]);
+                    if (BIAS)
+                        db[v][e] += g[v][e];
+                    g[v][e] *= w[e];
+                    s[0] = fmaf(g[v][e], y[v][e], s[0]);
+                    s[1] += g[v][e];
+                }
+            }
+        row_sum<2>(s, tpr, red, turn);
+        const float mgy = s[0] * inv, mg = LAYER ? s[1] * inv : 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (live && in[v]) {
+                const int64_t at = row * a.dim + (lane_r + v * tpr) * E;
+                float d[E], o[E];
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    d[e] = 0.f;
+                if (a.dres_out)
+                    load_row<R, E>(static_cast<const R *>(a.dres_out) + at, d);
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    g[v][e] = fmaf(k, fmaf(-y[v][e], mgy, g[v][e] - mg), d[e]);
+                    o[e] = a.alpha * g[v][e];
+                }
+                if (a.dres)
+                    store_row<R, E>(static_cast<R *>(a.dres) + at, o);
+            }
+        if (SCALE || POST) {
+            float t[NV][E];   // x, normed with POST
+#pragma unroll
+            for (int v = 0; v < NV; v++) {
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    t[v][e] = 0.f;
+                if (live && in[v])
+                    Vec<T>::load(static_cast<const T *>(a.x) + row * a.dim + (lane_r + v * tpr) * E, t[v]);
+            }
+            float p = 1.f;
+            if (POST) {
+                float q[1] = {0.f};
+#pragma unroll
+                for (int v = 0; v < NV; v++)
+#pragma unroll
+                    for (int e = 0; e < E; e++)
+                        q[0] = fmaf(t[v][e], t[v][e], q[0]);
+                row_sum<1>(q, tpr, red, turn);
+                p = rsqrtf(q[0] * inv + a.eps);
+            }
+            float se[1] = {0.f};   // sum of e x p
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+                if (live && in[v]) {
+                    const int c = (lane_r + v * tpr) * E;
+                    float w[E];
+                    if (POST) {
+                        load_f32<E>(a.post + c, w);
+#pragma unroll
+                        for (int e = 0; e < E; e++)
+                            t[v][e] *= p;
+                    }
+                    if (SCALE) {
+                        float sc[E];
+                        load_f32<E>(a.scale + set * a.dim + c, sc);
+#pragma unroll
+                        for (int e = 0; e < E; e++) {
+                            dsc[v][e] = fmaf(g[v][e], POST ? t[v][e] * w[e] : t[v][e], dsc[v][e]);
+                            g[v][e] *= sc[e];
+                        }
+                    }
+                    if (POST)
+#pragma unroll
+                        for (int e = 0; e < E; e++) {
+                            dpo[v][e] = fmaf(g[v][e], t[v][e], dpo[v][e]);
+                            g[v][e] *= w[e];
+                            se[0] = fmaf(g[v][e], t[v][e], se[0]);
+                        }
+                }
+            if (POST) {
+                row_sum<1>(se, tpr, red, turn);
+                const float me = se[0] * inv;
+#pragma unroll
+                for (int v = 0; v < NV; v++)
+#pragma unroll
+                    for (int e = 0; e < E; e++)
+                        g[v][e] = p * fmaf(-t[v][e], me, g[v][e]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+            if (live && in[v])
+                Vec<T>::store(static_cast<T *>(a.dx) + row * a.dim + (lane_r + v * tpr) * E, g[v]);
+    }
+    // partial column sums: kind after kind, (sets, parts, dim) each
+    float *out = a.parts + (size_t)blockIdx.x * a.dim;
+    const size_t kind = (size_t)gridDim.x * a.dim;
+    auto put = [&](const float(&d)[NV][E]) {
+        for (int s = 0; s < rpb; s++) {
+            if (s == sub)
+#pragma unroll
+                for (int v = 0; v < NV; v++)
+                    if (in[v])
+#pragma unroll
+                        for (int e = 0; e < E; e++) {
+                            const int c = (lane_r + v * tpr) * E + e;
+                            cols[c] = s == 0 ? d[v][e] : cols[c] + d[v][e];
+                        }
+            __syncthreads();
+        }
+        for (int c = threadIdx.x; c < a.dim; c += blockDim.x)
+            out[c] = cols[c];
+        __syncthreads();
+        out += kind;
+    };
+    put(dw);
+    if constexpr (BIAS)
+        put(db);
+    if constexpr (SCALE)
+        put(dsc);
+    if constexpr (POST)
+        put(dpo);
+}
+
+template <typename T, typename R> cudaError_t fwd_typed(const ResidualArgs &a, cudaStream_t st)
+{
+    const NormPlan p = residual_plan(a.rows, 1, a.dim);
+    if (a.layer)
+        residual_fwd_kernel<T, R, true><<<p.parts, p.threads, 0, st>>>(a, p.tpr, p.rows_at_once);
+    else
+        residual_fwd_kernel<T, R, false><<<p.parts, p.threads, 0, st>>>(a, p.tpr, p.rows_at_once);
+    return cudaGetLastError();
+}
+
+template <typename T, typename R> cudaError_t bwd_typed(const ResidualArgs &a, cudaStream_t st)
+{
+    const int64_t sets = row_sets(a.samples, a.scale != nullptr);
+    const NormPlan p = residual_plan(a.rows, sets, a.dim);
+    const unsigned blocks = (unsigned)(sets * p.parts);
+    auto go = [&](auto layer, auto bias, auto scale, auto post) {
+        residual_bwd_kernel<T, R, layer.value, bias.value, scale.value, post.value>
+            <<<blocks, p.threads, a.dim * sizeof(float), st>>>(a, p.tpr, p.rows_at_once, p.parts);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    auto post = [&](auto l, auto b, auto s) { a.post ? go(l, b, s, yes) : go(l, b, s, no); };
+    auto scale = [&](auto l, auto b) { a.scale ? post(l, b, yes) : post(l, b, no); };
+    auto bias = [&](auto l) { a.bias ? scale(l, yes) : scale(l, no); };
+    a.layer ? bias(yes) : bias(no);
+    cudaError_t e = cudaGetLastError();
+    const float *part = a.parts;
+    const size_t kind = (size_t)blocks * a.dim;
+    auto sum = [&](float *out, int64_t n) {   // n sets of rows, or all of them together
+        if (e == cudaSuccess)
+            e = launch_part_sum(part, n, (int)(blocks / n), a.dim, out, st);
+        part += kind;
+    };
+    sum(a.dweight, 1);
+    if (a.bias)
+        sum(a.dbias, 1);
+    if (a.scale)
+        sum(a.dscale, sets);
+    if (a.post)
+        sum(a.dpost, 1);
+    return e;
+}
+
+}  // namespace
+
+size_t residual_bwd_workspace(int64_t rows, int64_t samples, int dim, bool has_bias, bool has_scale, bool has_post)
+{
+    const int64_t sets = row_sets(samples, has_scale);
+    const size_t kinds = 1 + has_bias + has_scale + has_post;
+    return kinds * (size_t)sets * residual_plan(rows, sets, dim).parts * dim * sizeof(float);
+}
+
+cudaError_t launch_residual_fwd(const ResidualArgs &a, cudaStream_t st)
+{
+    if (a.dtype == 0)
+        return fwd_typed<float, float>(a, st);
+    return a.res32 ? fwd_typed<__nv_bfloat16, float>(a, st) : fwd_typed<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_residual_bwd(const ResidualArgs &a, cudaStream_t st)
+{
+    if (a.dtype == 0)
+        return bwd_typed<float, float>(a, st);
+    return a.res32 ? bwd_typed<__nv_bfloat16, float>(a, st) : bwd_typed<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+}  // namespace ssm
