@@ -1,0 +1,718 @@
+// gdr_chunk.cu -- the gated delta rule over sequences, chunk by chunk on the
+// tensor cores (tcgen05, TMA, tensor memory).
+//
+// With q~ = scale q / |q|, k^ = k / |k| and, in a chunk of 64 steps,
+// cs = the inclusive sum of the log decays (base 2), G_ij = 2^(cs_i - cs_j),
+// c_i = 2^cs_i, e_j = 2^(cs_end - cs_j), the steps of a chunk together are
+//     A_ij = b_i G_ij k^_i.k^_j  (j < i),   T = (I + A)^-1,   P = G o (Q~ K^T)  (j <= i)
+//     N = T diag(b) (V - diag(c) K^ S^T)
+//     O = diag(c) Q~ S^T + P N
+//     S = c_end S + N^T diag(e) K^
+// One block owns one (batch, value head) and walks its chunks; only S passes
+// on.  Everything is kept transposed, value channels down: lane v of tensor
+// memory and of the state's threads is row v of S (V, K), so S, N^T and O^T
+// go from one product to the next as A operands in tensor memory, written by
+// the thread that read their accumulator, with no exchange between threads.
+// The norms of q and k, b and all decays are scalars of a row or column and
+// stay outside the products: K, Q and V are read as they came.
+//
+// Roundings: K, Q are exact bf16; S, diag(b)(V - ..), T and N enter the
+// products that lead to the state as bf16 pairs hi + lo (at least 16 bits;
+// S K^T and N^T K two products, T .. three), so the state, float32 in
+// registers between chunks, is good to about 2^-17 per product; P, and N and
+// S on the way to the outputs, are single bf16 (out is rounded to bf16
+// anyway).  T is inverted with float32 in its 16 x 16 diagonal blocks and
+// bf16 pairs between them.
+//
+// Per chunk the state's dependence runs S -> S K^T -> (V - ..) -> T .. -> N ->
+// N^T K -> S: four products of the tensor core with a pass of 256 threads
+// after each.  The two halves of S's columns (K = 128) are handed on one by
+// one, so their passes overlap with products.  Beside it, for the chunks
+// ahead, two teams of four warps in turn build P and T from K K^T and Q K^T
+// (one product), a loader brings the tiles of K, Q, V (TMA, three stages) and
+// the log decays, and the outputs of a chunk are read while the next chunk's
+// first product runs.
+#include <type_traits>
+
+#include "gdr_math.cuh"
+#include "tc100.cuh"
+
+namespace ssm {
+
+__device__ unsigned g_gdr_error;
+__device__ long long g_probe[64][64];
+#define PROBE(k) do { if (blockIdx.x == 0 && lane == 0 && c < 64) g_probe[c][k] = clock64(); } while (0)
+   // a bounded wait gave up
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kC = 64;                        // steps per chunk
+constexpr int kStages = 3;
+constexpr int kTile = kC * 128;               // 64 rows of 64 bf16
+constexpr int kStageBytes = 6 * kTile;        // K, Q (first halves), K, Q (second halves), V, V
+constexpr int kOffV = 4 * kTile;
+constexpr int kOffP = kStages * kStageBytes;  // P: rows of 64, K-major
+constexpr int kOffT = kOffP + kStages * kTile;   // T hi, lo; A off the diagonal before it
+constexpr int kOffVec = kOffT + kStages * 2 * kTile;
+struct Vec {               // of one chunk
+    float2 csk[kC];        // cs, 1 / |k|
+    float2 bg[kC];         // b, -b c / |k|
+    float gq[kC];          // c scale / |q|
+    float ek[kC];          // e / |k|
+    float b[kC];
+    float dec;             // 2^cs_end
+    float pad[3];
+};
+
+// tensor memory columns.  S: per 16 columns of the state 8 of bf16 pairs hi
+// and 8 lo, in place of the 16 float32 that N^T K leaves there
+constexpr uint32_t kColS = 0;      // 128
+constexpr uint32_t kColKS = 128;   // 64: S K^T, then N
+constexpr uint32_t kColQS = 192;   // 64
+constexpr uint32_t kColPN = 256;   // 64
+constexpr uint32_t kColKK = 320;   // 64: lanes 0..63 K K^T, 64..127 Q K^T
+constexpr uint32_t kColX = 384;    // 64: hi 32, lo 32 of diag(b)(V - ..), then of N diag(e)
+constexpr uint32_t kColN = 448;    // 32: N, one bf16
+constexpr int kTmemCols = 512;
+
+constexpr int kStateWarps = 8, kPrepWarp = 8, kMmaWarp = 16, kLoadWarp = 17, kThreads = 20 * 32;
+// Registers: launched with 96 a thread (61,440 in all); the last four warps
+// (products, loads, two idle) give up 56 x 128, the state's eight take 24 x 256.
+constexpr int kRegsState = 120, kRegsIssue = 40;
+
+struct Bars {
+    uint64_t full[kStages], scal[kStages], ready[kStages], empty[kStages];
+    uint64_t s[2], ks, d, t, n, x[2], o, oread, kk[2], kkread, team[2][3], done;   // kk: one for each team
+    uint32_t tmem;
+    int abort;
+};
+constexpr int kOffBars = kOffVec + kStages * (int)sizeof(Vec);
+constexpr int kSmem = kOffBars + (int)sizeof(Bars);
+static_assert(kSmem <= 227 * 1024, "shared memory of one block");
+
+template <int K>
+__global__ void __launch_bounds__(kThreads, 1)
+    gdr_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                     const __grid_constant__ CUtensorMap mapV, const GdrArgs a, const int nch)
+{
+    using namespace tc;
+    constexpr int KH = K / 2;             // columns of S of one half of the state's threads
+    constexpr int kSteps = K / 16;
+    // used as declared (no arithmetic on its address), so that the compiler
+    // knows every access for one to shared memory
+    extern __shared__ __align__(1024) uint8_t sm[];
+    Bars &bars = *reinterpret_cast<Bars *>(sm + kOffBars);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t bh = blockIdx.x;
+    const int h = (int)(bh % a.Hv), hk = h / (a.Hv / a.Hk);
+    const int b = (int)(bh / a.Hv);
+    const int L = a.L, V = a.V;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; i++) {
+            bar_init(&bars.full[i], 1);
+            bar_init(&bars.scal[i], 32);
+            bar_init(&bars.ready[i], 4);
+            bar_init(&bars.empty[i], 1 + kStateWarps);
+        }
+        for (int i = 0; i < 2; i++) {
+            bar_init(&bars.s[i], kStateWarps / 2);
+            bar_init(&bars.x[i], 1);
+            bar_init(&bars.kk[i], 1);
+            for (int j = 0; j < 3; j++)
+                bar_init(&bars.team[i][j], 4);
+        }
+        bar_init(&bars.ks, 1);
+        bar_init(&bars.d, kStateWarps);
+        bar_init(&bars.t, 1);
+        bar_init(&bars.n, kStateWarps);
+        bar_init(&bars.o, 1);
+        bar_init(&bars.oread, kStateWarps);
+        bar_init(&bars.kkread, 4);
+        bar_init(&bars.done, 1);
+        bars.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0)
+        tmem_alloc(&bars.tmem, kTmemCols);
+    // T stays zero above its diagonal blocks
+    for (int i = tid; i < kStages * 2 * kTile / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(sm + kOffT)[i] = make_uint4(0, 0, 0, 0);
+    fence_smem();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = bars.tmem;
+    volatile int *abort = &bars.abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, &g_gdr_error); };
+    auto stage = [&](int c) { return sm + (c % kStages) * kStageBytes; };
+    auto vec = [&](int c) { return reinterpret_cast<Vec *>(sm + kOffVec) + c % kStages; };
+    auto phase = [](int c) { return (uint32_t)((c / kStages) & 1); };
+    auto arrive1 = [&](uint64_t *bar) {   // one arrival of this warp, after all its lanes
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(bar);
+    };
+
+    if (warp < kStateWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsState));
+        // ---- the state's threads: lane row v, half `half` of K's columns and of a chunk's steps
+        const int half = warp >> 2, v = (warp & 3) * 32 + lane;
+        const bool live = (warp & 3) * 32 < V;   // V = 64: half of the warps only keep step
+        const uint32_t tl = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        float S[KH];
+        const size_t srow = ((size_t)bh * V + v) * K + half * KH;
+        if (live && a.init) {
+#pragma unroll
+            for (int i = 0; i < KH; i += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(a.init + srow + i);
+                S[i] = f.x, S[i + 1] = f.y, S[i + 2] = f.z, S[i + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < KH; i++)
+                S[i] = 0.f;
+        }
+        auto put_S = [&](int p) {   // 16 columns of S as an operand
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                split(S[16 * p + 2 * i], S[16 * p + 2 * i + 1], hi[i], lo[i]);
+            tmem_st(tl + kColS + half * KH + 16 * p, hi);
+            tmem_st(tl + kColS + half * KH + 16 * p + 8, lo);
+        };
+        if (live) {
+#pragma unroll
+            for (int p = 0; p < KH / 16; p++)
+                put_S(p);
+            tmem_wait_st();
+        }
+        fence_before();
+        arrive1(&bars.s[half]);
+        const uint32_t vrow = kOffV + (v >= 64 ? kTile : 0) + (v & 7) * 2;
+        const int vpiece = (v >> 3) & 7;
+        bf16 *out = static_cast<bf16 *>(a.out) + ((size_t)b * L * a.Hv + h) * V + v;
+        for (int c = 0; c < nch; c++) {
+            const Vec *ve = vec(c);
+            if (warp==0) PROBE(0);
+            // 1. diag(b)(V - diag(c) K^ S^T), this half's 32 steps
+            if (!wait(&bars.full[c % kStages], phase(c)) || !wait(&bars.ready[c % kStages], phase(c)) ||
+                !wait(&bars.ks, c & 1))
+                break;
+            fence_after();
+            if (warp==0) PROBE(1);
+            if (live) {
+                const uint8_t *vt = stage(c) + vrow;
+#pragma unroll
+                for (int p = 0; p < 2; p++) {
+                    uint32_t r[16], hi[8], lo[8];
+                    tmem_ld(tl + kColKS + 32 * half + 16 * p, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const int s = 32 * half + 16 * p + 2 * i;
+                        const float4 bg = *reinterpret_cast<const float4 *>(&ve->bg[s]);   // of two steps
+                        const float v0 = __bfloat162float(*reinterpret_cast<const bf16 *>(vt + s * 128 + ((vpiece ^ (s & 7)) << 4)));
+                        const float v1 = __bfloat162float(
+                            *reinterpret_cast<const bf16 *>(vt + (s + 1) * 128 + ((vpiece ^ ((s + 1) & 7)) << 4)));
+                        split(fmaf(bg.y, __uint_as_float(r[2 * i]), bg.x * v0),
+                              fmaf(bg.w, __uint_as_float(r[2 * i + 1]), bg.z * v1), hi[i], lo[i]);
+                    }
+                    tmem_st(tl + kColX + 16 * half + 8 * p, hi);
+                    tmem_st(tl + kColX + 32 + 16 * half + 8 * p, lo);
+                }
+                tmem_wait_st();
+            }
+            fence_before();
+            arrive1(&bars.d); if (warp==0) PROBE(2);
+            // 2. N, and N diag(e) for the state
+            if (!wait(&bars.t, c & 1))
+                break;
+            fence_after(); if (warp==0) PROBE(3);
+            if (live) {
+#pragma unroll
+                for (int p = 0; p < 2; p++) {
+                    uint32_t r[16], hi[8], lo[8], one[8];
+                    tmem_ld(tl + kColKS + 32 * half + 16 * p, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float2 e = *reinterpret_cast<const float2 *>(&ve->ek[32 * half + 16 * p + 2 * i]);
+                        const float n0 = __uint_as_float(r[2 * i]), n1 = __uint_as_float(r[2 * i + 1]);
+                        one[i] = pack(n0, n1);
+                        split(n0 * e.x, n1 * e.y, hi[i], lo[i]);
+                    }
+                    tmem_st(tl + kColX + 16 * half + 8 * p, hi);
+                    tmem_st(tl + kColX + 32 + 16 * half + 8 * p, lo);
+                    tmem_st(tl + kColN + 16 * half + 8 * p, one);
+                }
+                tmem_wait_st();
+            }
+            fence_before();
+            arrive1(&bars.n); if (warp==0) PROBE(4);
+            // 3. S = c_end S + N^T diag(e) K^, this half's columns
+            if (!wait(&bars.x[half], c & 1))
+                break;
+            fence_after(); if (warp==0) PROBE(5);if (warp==4) PROBE(30);
+            if (live) {
+                const float dec = ve->dec;
+#pragma unroll
+                for (int p = 0; p < KH / 16; p++) {
+                    uint32_t r[16];
+                    tmem_ld(tl + kColS + half * KH + 16 * p, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        S[16 * p + i] = fmaf(dec, S[16 * p + i], __uint_as_float(r[i]));
+                    put_S(p);
+                }
+                tmem_wait_st();
+            }
+            fence_before();
+            arrive1(&bars.s[half]); if (warp==0) PROBE(6);if (warp==4) PROBE(31);
+            // 4. outputs of this half's steps
+            if (!wait(&bars.o, c & 1))
+                break;
+            fence_after(); if (warp==0) PROBE(7);
+            if (live) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    uint32_t q[16], p[16];
+                    tmem_ld(tl + kColQS + 32 * half + 16 * j, q);
+                    tmem_ld(tl + kColPN + 32 * half + 16 * j, p);
+                    tmem_wait(q);
+                    tmem_wait(p);
+                    const int s0 = 32 * half + 16 * j, t0 = c * kC + s0;
+                    bf16 *o = out + (size_t)t0 * a.Hv * V;
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        if (t0 + i < L)
+                            o[(size_t)i * a.Hv * V] =
+                                __float2bfloat16_rn(fmaf(ve->gq[s0 + i], __uint_as_float(q[i]), __uint_as_float(p[i])));
+                }
+            }
+            fence_before();
+            arrive1(&bars.oread); if (warp==0) PROBE(8);
+            arrive1(&bars.empty[c % kStages]);
+        }
+        if (live && a.last && !*abort) {
+#pragma unroll
+            for (int i = 0; i < KH; i += 4)
+                *reinterpret_cast<float4 *>(a.last + srow + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+        }
+    } else if (warp < kMmaWarp) {
+        // ---- the teams that build P, T and the scalars: thread = row of K (0..63) or of Q
+        const int team = (warp - kPrepWarp) >> 2, pw = warp & 3;
+        const int row = pw * 32 + lane;          // lane of tensor memory
+        const bool isq = pw >= 2;
+        const int i = row & 63;                  // step in the chunk
+        const uint32_t tl = tm + ((uint32_t)(pw * 32) << 16);
+        int turn = 0;
+        for (int c = team; c < nch; c += 2, turn++) {
+            Vec *ve = vec(c);
+            const uint8_t *st = stage(c);
+            uint8_t *Pb = sm + kOffP + (c % kStages) * kTile, *Tb = sm + kOffT + (c % kStages) * 2 * kTile;
+            const uint32_t tb = smem_u32(Tb);
+            if (!wait(&bars.scal[c % kStages], phase(c)) || !wait(&bars.full[c % kStages], phase(c)))
+                break;
+            if (pw==1) PROBE(10);
+            float norm = 1.f;   // 1 / |k| or 1 / |q| of this thread's row
+            if (a.l2norm) {
+                float s = 0.f;
+#pragma unroll
+                for (int f = 0; f < K / 64; f++)
+#pragma unroll
+                    for (int p = 0; p < 8; p++) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(st + (2 * f + isq) * kTile + sw128(i, p));
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            s = fmaf(lo_f(w[e]), lo_f(w[e]), fmaf(hi_f(w[e]), hi_f(w[e]), s));
+                    }
+                norm = rsqrtf(s + kL2Eps);
+            }
+            const float csi = ve->csk[i].x;
+            if (!isq)
+                ve->csk[i].y = norm;
+            arrive1(&bars.team[team][0]);
+            if (!wait(&bars.team[team][0], turn & 1) || !wait(&bars.kk[team], turn & 1))
+                break;
+            fence_after();
+            if (pw==1) PROBE(11);
+            const float f = isq ? a.scale * norm : norm * ve->b[i];   // the row's factor
+            const int last = isq ? i : i - 1, blk = i >> 4, il = i & 15;
+            // rows of 16 as bf16 pairs: A left of the diagonal block, that block's inverse in it
+            auto put = [&](int at_blk, const float (&x)[16]) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    split(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    const uint32_t at = sw128(i, 2 * at_blk + q);
+                    *reinterpret_cast<uint4 *>(Tb + at) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                    *reinterpret_cast<uint4 *>(Tb + kTile + at) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                }
+            };
+            float d[16];   // this row of the diagonal block of A
+#pragma unroll
+            for (int p = 0; p < 4; p++) {
+                float w[16];
+                if (16 * p <= (pw & 1) * 32 + 31) {   // same for the warp: some row reaches these columns
+                    uint32_t r[16];
+                    tmem_ld(tl + kColKK + 16 * p, r);
+                    tmem_wait(r);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float4 ck = *reinterpret_cast<const float4 *>(&ve->csk[16 * p + j]);
+                        const float g0 = ex2_mufu(csi - ck.x) * ck.y * f, g1 = ex2_mufu(csi - ck.z) * ck.w * f;
+                        w[j] = 16 * p + j <= last ? __uint_as_float(r[j]) * g0 : 0.f;
+                        w[j + 1] = 16 * p + j + 1 <= last ? __uint_as_float(r[j + 1]) * g1 : 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        w[j] = 0.f;
+                }
+                if (isq) {
+#pragma unroll
+                    for (int q = 0; q < 2; q++)
+                        *reinterpret_cast<uint4 *>(Pb + sw128(i, 2 * p + q)) =
+                            make_uint4(pack(w[8 * q], w[8 * q + 1]), pack(w[8 * q + 2], w[8 * q + 3]),
+                                       pack(w[8 * q + 4], w[8 * q + 5]), pack(w[8 * q + 6], w[8 * q + 7]));
+                } else {
+                    if (p < blk)
+                        put(p, w);
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        d[j] = p == blk ? w[j] : (p == 0 ? 0.f : d[j]);
+                }
+            }
+            fence_before();
+            arrive1(&bars.kkread); if (pw==1) PROBE(12);
+            if (!isq) {
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 16; j++)
+                    x[j] = 0.f;
+                // row il of the inverse of I + D from the right: x_k is final once all
+                // later ones are, then leaves -x_k D_kj in the columns j < k
+#pragma unroll
+                for (int k = 15; k >= 0; k--) {
+                    x[k] = k == il ? 1.f : x[k];
+#pragma unroll
+                    for (int j = 0; j < k; j++)
+                        x[j] = fmaf(-x[k], __shfl_sync(0xffffffffu, d[j], (lane & 16) | k), x[j]);
+                }
+                put(blk, x);
+            }
+            if (pw==1) PROBE(13); arrive1(&bars.team[team][1]);
+            if (!wait(&bars.team[team][1], turn & 1))
+                break;
+            // block row pw of T: T_ij = -(sum_{j < k <= i} T_ik A_kj) T_jj, as A operands of the next sums
+            if (pw==3) PROBE(14);
+            uint32_t th[4][4], tlo[4][4];
+            const uint32_t aoff = (lane & 7) + ((lane >> 3) & 1) * 8;
+            auto load_a = [&](int bi, int bj, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+                const uint32_t at = tb + sw128(16 * bi + aoff, 2 * bj + (lane >> 4));
+                ldsm(at, hi);
+                ldsm(at + kTile, lo);
+            };
+            auto load_b = [&](int bi, int bj, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+                const uint32_t at = tb + sw128(16 * bi + aoff, 2 * bj + (lane >> 4));
+                ldsm_t(at, hi);
+                ldsm_t(at + kTile, lo);
+            };
+            auto prod = [&](float (&acc)[2][4], const uint32_t (&ah)[4], const uint32_t (&al)[4], const uint32_t (&bh_)[4],
+                            const uint32_t (&bl)[4]) {
+#pragma unroll
+                for (int n = 0; n < 2; n++) {
+                    mma16816(acc[n], ah, bh_[2 * n], bh_[2 * n + 1]);
+                    mma16816(acc[n], ah, bl[2 * n], bl[2 * n + 1]);
+                    mma16816(acc[n], al, bh_[2 * n], bh_[2 * n + 1]);
+                }
+            };
+            auto as_a = [&](const float (&acc)[2][4], float sign, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+                split(sign * acc[0][0], sign * acc[0][1], hi[0], lo[0]);
+                split(sign * acc[0][2], sign * acc[0][3], hi[1], lo[1]);
+                split(sign * acc[1][0], sign * acc[1][1], hi[2], lo[2]);
+                split(sign * acc[1][2], sign * acc[1][3], hi[3], lo[3]);
+            };
+            auto row_of_T = [&](auto I) {
+                constexpr int bi = decltype(I)::value;
+                load_a(bi, bi, th[bi], tlo[bi]);
+#pragma unroll
+                for (int j = bi - 1; j >= 0; j--) {
+                    float acc[2][4] = {}, res[2][4] = {};
+                    uint32_t bh_[4], bl[4], mh[4], ml[4];
+#pragma unroll
+                    for (int k = bi; k > j; k--) {
+                        load_b(k, j, bh_, bl);
+                        prod(acc, th[k], tlo[k], bh_, bl);
+                    }
+                    as_a(acc, -1.f, mh, ml);
+                    load_b(j, j, bh_, bl);
+                    prod(res, mh, ml, bh_, bl);
+                    as_a(res, 1.f, th[j], tlo[j]);
+                }
+            };
+            if (pw == 0) {   // no blocks left of the first: the scalars instead
+                const float end = ve->csk[kC - 1].x;
+#pragma unroll
+                for (int s = 0; s < 2; s++) {
+                    const int at = lane + 32 * s;
+                    const float2 ck = ve->csk[at];
+                    const float bb = ve->b[at], cd = ex2_mufu(ck.x);
+                    ve->bg[at] = make_float2(bb, -bb * cd * ck.y);
+                    ve->ek[at] = ex2_mufu(end - ck.x) * ck.y;
+                }
+                if (lane == 0)
+                    ve->dec = ex2_mufu(end);
+            } else if (pw == 1) {
+                row_of_T(std::integral_constant<int, 1>());
+            } else if (pw == 2) {
+                row_of_T(std::integral_constant<int, 2>());
+            } else {
+                row_of_T(std::integral_constant<int, 3>());
+            }
+            if (isq)
+                ve->gq[i] = ex2_mufu(csi) * f;
+            if (pw==3) PROBE(15); arrive1(&bars.team[team][2]);
+            if (!wait(&bars.team[team][2], turn & 1))   // nobody reads A any more
+                break;
+#pragma unroll
+            for (int j = 0; j < 3; j++)
+                if (j < pw)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const uint32_t at = sw128(16 * pw + (lane >> 2) + 8 * (e & 1), 2 * j + (e >> 1)) + (lane & 3) * 4;
+                        *reinterpret_cast<uint32_t *>(Tb + at) = th[j][e];
+                        *reinterpret_cast<uint32_t *>(Tb + kTile + at) = tlo[j][e];
+                    }
+            fence_smem();
+            arrive1(&bars.ready[c % kStages]); if (pw==3) PROBE(16);
+        }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (warp == kMmaWarp) {
+        // ---- one lane issues every product of the chain
+        constexpr uint32_t id64 = idesc(128, 64, 0, 0);       // B: rows of 64 steps, K-major
+        constexpr uint32_t idUp = idesc(128, 64, 0, 1);       // B: K itself, steps along K
+        auto issue_kk = [&](int c) {
+            const uint32_t s = smem_u32(stage(c));
+            if (lane == 0) {
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < kSteps; k++) {
+                    const uint64_t o = operand(s + (k >> 2) * 2 * kTile + (k & 3) * 32);
+                    mma_ss(tm + kColKK, o, o, id64, k > 0);
+                }
+                commit(&bars.kk[c & 1]);
+            }
+            __syncwarp();
+        };
+        bool ok = true;
+        int next_kk = 0;   // the next chunk whose K K^T is to be issued
+        auto kk_blocking = [&] {
+            if (next_kk >= nch)
+                return true;
+            if (!wait(&bars.full[next_kk % kStages], phase(next_kk)) ||
+                (next_kk > 0 && !wait(&bars.kkread, (next_kk - 1) & 1)))
+                return false;
+            issue_kk(next_kk++);
+            return true;
+        };
+        ok = kk_blocking() && kk_blocking();
+        for (int c = 0; c < nch && ok; c++) {
+            const uint32_t s = smem_u32(stage(c));
+            const uint32_t T = smem_u32(sm + kOffT + (c % kStages) * 2 * kTile), P = smem_u32(sm + kOffP + (c % kStages) * kTile);
+            // S K^T (hi + lo), a half of S's columns at a time
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                ok = wait(&bars.s[half], c & 1);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    fence_after();
+#pragma unroll
+                    for (int k = half * kSteps / 2; k < (half + 1) * kSteps / 2; k++) {
+                        const uint64_t kd = operand(s + (k >> 2) * 2 * kTile + (k & 3) * 32);
+                        mma_ts(tm + kColKS, tm + kColS + 16 * k, kd, id64, k > 0);
+                        mma_ts(tm + kColKS, tm + kColS + 16 * k + 8, kd, id64, true);
+                    }
+                    if (half == 1)
+                        commit(&bars.ks);
+                }
+                __syncwarp();
+            }
+            PROBE(20);
+            if (!ok || (c > 0 && !wait(&bars.oread, (c - 1) & 1)))
+                break;
+            if (lane == 0) {
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < kSteps; k++)
+                    mma_ts(tm + kColQS, tm + kColS + 16 * k, operand(s + ((k >> 2) * 2 + 1) * kTile + (k & 3) * 32), id64,
+                           k > 0);
+            }
+            __syncwarp();
+            if (next_kk == c + 1 && !kk_blocking())
+                break;
+            PROBE(21);
+            // N = T (..): hi hi, hi lo, lo hi
+            if (!wait(&bars.ready[c % kStages], phase(c)) || !wait(&bars.d, c & 1))
+                break;
+            if (lane == 0) {
+                fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    mma_ts(tm + kColKS, tm + kColX + 8 * k, operand(T + k * 32), id64, k > 0);
+                    mma_ts(tm + kColKS, tm + kColX + 8 * k, operand(T + kTile + k * 32), id64, true);
+                    mma_ts(tm + kColKS, tm + kColX + 32 + 8 * k, operand(T + k * 32), id64, true);
+                }
+                commit(&bars.t);
+            }
+            __syncwarp();
+            PROBE(22);
+            if (!wait(&bars.n, c & 1))
+                break;
+            if (lane == 0) {
+                fence_after();
+#pragma unroll
+                for (int f = 0; f < K / 64; f++) {   // 64 columns of N^T diag(e) K^ (hi + lo) in S's place
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint64_t kd = operand(s + f * 2 * kTile + k * 2048);
+                        mma_ts(tm + kColS + 64 * f, tm + kColX + 8 * k, kd, idUp, k > 0);
+                        mma_ts(tm + kColS + 64 * f, tm + kColX + 32 + 8 * k, kd, idUp, true);
+                    }
+                    commit(&bars.x[f]);
+                }
+                if (K == 64)
+                    commit(&bars.x[1]);
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    mma_ts(tm + kColPN, tm + kColN + 8 * k, operand(P + k * 32), id64, k > 0);
+                commit(&bars.o);
+                commit(&bars.empty[c % kStages]);
+            }
+            __syncwarp();
+            PROBE(23);
+            // the product for the chunk after next, if its tiles are here (else after the next S K^T)
+            if (next_kk == c + 2 && next_kk < nch &&
+                __all_sync(0xffffffffu, bar_test(&bars.full[next_kk % kStages], phase(next_kk)) &&
+                                            bar_test(&bars.kkread, (next_kk - 1) & 1)))
+                issue_kk(next_kk++);
+        }
+        if (lane == 0) {
+            commit(&bars.done);
+            drain(&bars.done, 0, &g_gdr_error);
+        }
+        __syncwarp();
+    } else if (warp == kLoadWarp) {
+        // ---- the loader: tiles, decays and b, up to three chunks ahead
+        const float bias = a.bias ? a.bias[h] : 0.f, Ah = a.A[h] * kLog2e;
+        const bf16 *dp = static_cast<const bf16 *>(a.delta) + (size_t)b * L * a.Hv + h;
+        const bf16 *bp = static_cast<const bf16 *>(a.beta) + (size_t)b * L * a.Hv + h;
+        int issued = -1;
+        float dl[2], be[2];
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int t = c * kC + 2 * lane + e;
+                dl[e] = c < nch && t < L ? gdr_ld(dp, (size_t)t * a.Hv) : 0.f;
+                be[e] = c < nch && t < L ? gdr_ld(bp, (size_t)t * a.Hv) : 0.f;
+            }
+        };
+        fetch(0);
+        for (int c = 0; c < nch; c++) {
+            float g[2], bb[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const bool in = c * kC + 2 * lane + e < L;
+                g[e] = in ? gdr_dt(dl[e], bias, a.softplus) * Ah : 0.f;
+                bb[e] = in ? (a.sigmoid ? gdr_sigmoid(be[e]) : be[e]) : 0.f;
+            }
+            fetch(c + 1);
+            float incl = g[0] + g[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o)
+                    incl += u;
+            }
+            if (c >= kStages && !wait(&bars.empty[c % kStages], phase(c - kStages)))
+                break;
+            if (__any_sync(0xffffffffu, *abort))
+                break;
+            PROBE(40);
+            if (lane == 0) {
+                uint8_t *st = stage(c);
+                uint64_t *bar = &bars.full[c % kStages];
+                bar_expect(bar, (2 * (K / 64) + V / 64) * kTile);
+#pragma unroll
+                for (int f = 0; f < K / 64; f++) {
+                    tma_4d(st + 2 * f * kTile, &mapK, 64 * f, hk, c * kC, b, bar);
+                    tma_4d(st + (2 * f + 1) * kTile, &mapQ, 64 * f, hk, c * kC, b, bar);
+                }
+                for (int f = 0; f < V / 64; f++)
+                    tma_4d(st + kOffV + f * kTile, &mapV, 64 * f, h, c * kC, b, bar);
+            }
+            issued = c;
+            Vec *ve = vec(c);
+            ve->csk[2 * lane].x = incl - g[1];
+            ve->csk[2 * lane + 1].x = incl;
+            ve->b[2 * lane] = bb[0];
+            ve->b[2 * lane + 1] = bb[1];
+            bar_arrive(&bars.scal[c % kStages]);
+        }
+        if (lane == 0)
+            for (int c = max(0, issued - kStages + 1); c <= issued; c++)
+                drain(&bars.full[c % kStages], phase(c), &g_gdr_error);
+        __syncwarp();
+    }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 0)
+        tmem_free(tm, kTmemCols);
+}
+
+template <int K> cudaError_t launch(const GdrArgs &a, cudaStream_t st)
+{
+    CUtensorMap q, k, v;
+    if (!tc::head_map(&q, a.q, a.Bsz, a.L, a.Hk, a.K) || !tc::head_map(&k, a.k, a.Bsz, a.L, a.Hk, a.K) ||
+        !tc::head_map(&v, a.v, a.Bsz, a.L, a.Hv, a.V))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaFuncSetAttribute(gdr_chunk_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess)
+        return e;
+    gdr_chunk_kernel<K><<<(unsigned)((int64_t)a.Bsz * a.Hv), kThreads, kSmem, st>>>(q, k, v, a, (a.L + kC - 1) / kC);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t gdr_chunk_ws_bytes(const GdrArgs &) { return 0; }
+
+cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st)
+{
+    if (a.L < 16)
+        return launch_gdr_recurrent(a, st);
+    return a.K == 128 ? launch<128>(a, st) : launch<64>(a, st);
+}
+
+extern "C" void probe_read(long long *p) { cudaDeviceSynchronize(); cudaMemcpyFromSymbol(p, g_probe, sizeof(g_probe)); }
+cudaError_t read_and_clear_gdr_error(unsigned *value, cudaStream_t stream)
+{
+    cudaError_t e = cudaStreamSynchronize(stream);
+    if (e == cudaSuccess)
+        e = cudaMemcpyFromSymbol(value, g_gdr_error, sizeof(unsigned));
+    const unsigned zero = 0;
+    return e == cudaSuccess ? cudaMemcpyToSymbol(g_gdr_error, &zero, sizeof(unsigned)) : e;
+}
+
+}  // namespace ssm

@@ -27,6 +27,8 @@ cudaError_t launch_gdr_recurrent(const GdrArgs &a, cudaStream_t st);
 
 size_t gdr_chunk_ws_bytes(const GdrArgs &a);
 cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st);
+// The kernels' device-side error word (a bounded wait that gave up).
+cudaError_t read_and_clear_gdr_error(unsigned *value, cudaStream_t stream);
 
 struct GdrBwdArgs {
     GdrArgs f;

@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include "../../include/ssm.h"
+#include "gdr.h"
 #include "internal.h"
 
 namespace {
@@ -734,11 +735,12 @@ ssm_status ssd_chunk_fwd(const ssd_dims *dims, const void *x, const void *delta,
 
 ssm_status ssm_check_device(void *stream)
 {
-    unsigned v = 0, o = 0;
+    unsigned v = 0, g = 0, o = 0;
     if (ssm::read_and_clear_device_error(&v, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        ssm::read_and_clear_gdr_error(&g, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
         ssm::read_and_clear_s6_error(&o, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SSM_ERR_CUDA;
-    if (v)
+    if (v || g)
         return SSM_ERR_DEVICE_TIMEOUT;
     return o ? SSM_ERR_INVALID_ARG : SSM_OK;
 }

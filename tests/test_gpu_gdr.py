@@ -45,15 +45,16 @@ def f64(x, grad=False):
     return {n: ob.f64(t, grad) if isinstance(t, torch.Tensor) else t for n, t in x.items()}
 
 
-def close(got, want, f32):
+def close(got, want, f32, spread=1.0):
+    """spread: how much larger the root of the products' energy is, relative to the sum's, than twice (see above)."""
     g, o = host(got), want.detach().numpy()
     assert g.shape == o.shape
     if o.size == 0:
         return
     n = float((o * o).sum()) ** 0.5
     two = float(((g - o) ** 2).sum()) ** 0.5
-    assert two <= (2e-5 if f32 else 2 ** -7) * n + 1e-30, (two, n)
-    assert rel_err(g, o) <= (1e-4 if f32 else 2e-2)
+    assert two <= (2e-5 if f32 else 2 ** -7) * spread * n + 1e-30, (two, n)
+    assert rel_err(g, o) <= (1e-4 if f32 else 2e-2) * spread
 
 
 def run_fwd(x, flags):
@@ -118,14 +119,17 @@ def test_forward_ranges(cuda_device, name):
 
 @pytest.mark.parametrize("L", [96, 500])
 def test_forward_same_key_again(cuda_device, L):
-    """One key for every step, full strength: (I + A) is all ones below the diagonal."""
+    """One key for every step, full strength: (I + A) is all ones below the diagonal.
+    The state is then the last value alone, but a chunk adds it up from 64
+    terms v_j - v_(j-1) of twice that energy: 128 times the sum's where two
+    are assumed above, so the state may be off by the root of 64 times as much."""
     x = make(1, L, 1, 1, 128, 64, seed=5, beta=100.0, A=-0.01)
     x["k"][:] = x["k"][:, :1]
     x["q"][:] = x["k"]
     out, last = run_fwd(x, {})
     ro, rs = ob.gdr(**f64(x))
     close(out, ro, False)
-    close(last, rs, True)
+    close(last, rs, True, spread=8.0)
 
 
 def test_forward_zero_vectors(cuda_device):
