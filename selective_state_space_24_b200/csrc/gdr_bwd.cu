@@ -24,7 +24,15 @@
 // of E would: its diagonal, and all that does not cross t).
 // Sums over batch and length (dA, ddelta_bias) go through one partial sum per
 // chunk, added in a fixed order; the value heads of a key head are added in
-// one block.  All arithmetic is float32.
+// one block.
+//
+// Products run on the tensor cores as tf32 (mma.sync m16n8k8).  dA and
+// ddelta_bias are sums in which much cancels, so everything on the way to a
+// log decay's gradient keeps float32's precision: an operand is hi + lo, both
+// tf32 (11 bits each), and a product is hi hi + hi lo + lo hi; K, Q, V and dO
+// as they came are bf16 and exact in hi alone.  What only reaches bf16
+// results (dP, dA times K and Q) takes hi hi.  (Pairs of bf16 leave dA up to
+// 3e-5 off where the terms cancel.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -35,7 +43,7 @@ namespace ssm {
 namespace {
 
 constexpr int kC = 64;         // steps per chunk
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // eight warps: 2 x 4 over a 64-row tile
 constexpr int kSlice = 32;     // state rows of one chain block
 
 using bf16 = __nv_bfloat16;
@@ -44,317 +52,557 @@ using bf16 = __nv_bfloat16;
 struct Layout {
     int K, V, NC;
     int64_t heads;   // B Hv
-    __host__ __device__ size_t per() const
-    {
-        return (size_t)6 * kC + 2 * kC * kC + (size_t)kC * K + 3 * (size_t)kC * V + 2 * (size_t)V * K;
-    }
+    __host__ __device__ size_t per() const { return dS() + (size_t)V * K; }
     __host__ __device__ size_t base(int64_t bh, int n) const { return ((size_t)bh * NC + n) * per(); }
-    __host__ __device__ size_t cs() const { return 0; }                 // base-2 log decays, summed; then b
-    __host__ __device__ size_t rk() const { return 2 * kC; }            // factor of a row of k
-    __host__ __device__ size_t rq() const { return 3 * kC; }            // and of q (scale in it)
-    __host__ __device__ size_t T() const { return 6 * kC; }
-    __host__ __device__ size_t P() const { return T() + kC * kC; }
-    __host__ __device__ size_t W() const { return P() + kC * kC; }
-    __host__ __device__ size_t U() const { return W() + (size_t)kC * K; }
-    __host__ __device__ size_t N() const { return U() + (size_t)kC * V; }
-    __host__ __device__ size_t dN() const { return N() + (size_t)kC * V; }
+    __host__ __device__ size_t cs() const { return 0; }       // log decays (base 2), summed; then b
+    __host__ __device__ size_t rk() const { return 2 * kC; }  // factor of a row of k
+    __host__ __device__ size_t rq() const { return 3 * kC; }  // and of q (scale in it)
+    __host__ __device__ size_t T() const { return 4 * kC; }
+    __host__ __device__ size_t W() const { return T() + kC * kC; }
+    __host__ __device__ size_t U() const { return W() + (size_t)kC * K; }    // T diag(b) V, then N
+    __host__ __device__ size_t dN() const { return U() + (size_t)kC * V; }   // P^T dO, then dN
     __host__ __device__ size_t S0() const { return dN() + (size_t)kC * V; }
     __host__ __device__ size_t dS() const { return S0() + (size_t)V * K; }
 };
 
-// acc[i][j] += sum_k a(ty + 16 i, k) b(k, tx + 16 j)
-template <int RI, int RJ, class FA, class FB>
-__device__ __forceinline__ void mm(float (&acc)[RI][RJ], int n, FA a, FB b)
+// Pitches of shared tiles (in elements): a fragment's lanes read four
+// neighbouring k of eight rows, or eight neighbours of four rows; with these
+// either way is free of bank conflicts, or nearly.
+constexpr int pf(int n) { return n + 20; }   // float32
+constexpr int ph(int n) { return n + 8; }    // bf16
+constexpr int kPX = kC + 4;
+
+__device__ __forceinline__ float bf(const bf16 *p) { return __bfloat162float(*p); }
+
+__device__ __forceinline__ uint32_t tf32(float x)
 {
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    for (int k = 0; k < n; k++) {
-        float av[RI], bv[RJ];
-#pragma unroll
-        for (int i = 0; i < RI; i++)
-            av[i] = a(ty + 16 * i, k);
-#pragma unroll
-        for (int j = 0; j < RJ; j++)
-            bv[j] = b(k, tx + 16 * j);
-#pragma unroll
-        for (int i = 0; i < RI; i++)
-#pragma unroll
-            for (int j = 0; j < RJ; j++)
-                acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-    }
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
 }
-template <int RI, int RJ> __device__ __forceinline__ void zero(float (&acc)[RI][RJ])
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
 {
-#pragma unroll
-    for (int i = 0; i < RI; i++)
-#pragma unroll
-        for (int j = 0; j < RJ; j++)
-            acc[i][j] = 0.f;
-}
-template <int RI, int RJ, class F> __device__ __forceinline__ void each(float (&acc)[RI][RJ], F f)
-{
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-#pragma unroll
-    for (int i = 0; i < RI; i++)
-#pragma unroll
-        for (int j = 0; j < RJ; j++)
-            f(ty + 16 * i, tx + 16 * j, acc[i][j]);
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 
-// 64 rows of `cols` elements into shared memory (pitch cols + 1), zero from
-// row `valid` on
-__device__ __forceinline__ void load_rows(float *dst, const bf16 *src, size_t stride, int valid, int cols)
+// How an operand enters a product: two tf32 parts, one exact part (its values
+// are bf16), or one rounded part.
+enum Part { kTwo, kExact, kOne };
+
+template <Part P, int N> __device__ __forceinline__ void parts(const float (&x)[N], uint32_t (&hi)[N], uint32_t (&lo)[N])
 {
-    for (int x = threadIdx.x; x < kC * cols; x += kThreads) {
-        const int r = x / cols, c = x - r * cols;
-        dst[r * (cols + 1) + c] = r < valid ? __bfloat162float(src[r * stride + c]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        hi[i] = P == kExact ? __float_as_uint(x[i]) : tf32(x[i]);
+        lo[i] = P == kTwo ? __float_as_uint(x[i] - __uint_as_float(hi[i])) : 0u;
     }
 }
-__device__ __forceinline__ void load_f(float *dst, const float *src, int rows, int cols, int pitch, int ld)
+
+// A warp's tile: acc += a(m0 + .., k) b(k, n0 + ..), MT x 16 rows, NT x 8
+// columns.  Element e of acc[m][n] is row m0 + 16 m + lane / 4 + 8 (e / 2),
+// column n0 + 8 n + 2 (lane mod 4) + e mod 2.
+template <Part PA, Part PB, int MT, int NT, class FA, class FB>
+__device__ __forceinline__ void mm(float (&acc)[MT][NT][4], int m0, int n0, int kdim, FA a, FB b)
 {
-    for (int x = threadIdx.x; x < rows * cols; x += kThreads) {
-        const int r = x / cols, c = x - r * cols;
-        dst[r * pitch + c] = src[(size_t)r * ld + c];
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 2
+    for (int k = 0; k < kdim; k += 8) {
+        uint32_t ah[MT][4], al[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            const int r = m0 + 16 * m + g;
+            const float x[4] = {a(r, k + t), a(r + 8, k + t), a(r, k + t + 4), a(r + 8, k + t + 4)};
+            parts<PA>(x, ah[m], al[m]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const int c = n0 + 8 * n + g;
+            const float y[2] = {b(k + t, c), b(k + t + 4, c)};
+            uint32_t bh[2], bl[2];
+            parts<PB>(y, bh, bl);
+#pragma unroll
+            for (int m = 0; m < MT; m++) {
+                if (PB == kTwo)
+                    mma(acc[m][n], ah[m], bl);
+                if (PA == kTwo)
+                    mma(acc[m][n], al[m], bh);
+                mma(acc[m][n], ah[m], bh);
+            }
+        }
     }
 }
+template <int MT, int NT> __device__ __forceinline__ void zero(float (&acc)[MT][NT][4])
+{
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                acc[m][n][e] = 0.f;
+}
+// f(row, column, element) of every element this thread holds
+template <int MT, int NT, class F> __device__ __forceinline__ void each(float (&acc)[MT][NT][4], int m0, int n0, F f)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                f(m0 + 16 * m + g + 8 * (e >> 1), n0 + 8 * n + 2 * t + (e & 1), acc[m][n][e]);
+}
+// the same for pairs of neighbouring columns: f(row, column, first, second)
+template <int MT, int NT, class F> __device__ __forceinline__ void pairs(float (&acc)[MT][NT][4], int m0, int n0, F f)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < MT; m++)
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                f(m0 + 16 * m + g + 8 * h, n0 + 8 * n + 2 * t, acc[m][n][2 * h], acc[m][n][2 * h + 1]);
+}
+
+// Parts of the dot products of a tile's rows with rows of M: v[2 m + h] for row
+// m0 + 16 m + lane / 4 + 8 h.
+template <int NT, class F> __device__ __forceinline__ void dots(const float (&acc)[2][NT][4], int m0, int n0, F M, float (&v)[4])
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int m = 0; m < 2; m++)
+#pragma unroll
+        for (int q = 0; q < NT; q++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[2 * m + (e >> 1)] =
+                    fmaf(acc[m][q][e], M(m0 + 16 * m + g + 8 * (e >> 1), n0 + 8 * q + 2 * t + (e & 1)), v[2 * m + (e >> 1)]);
+}
+
+// 64 rows of N bf16 into shared memory, zero from row `valid` on (16 bytes at
+// a time; complete after cp_wait and a barrier)
+template <int N> __device__ __forceinline__ void load_rows(bf16 *dst, const bf16 *src, size_t stride, int valid)
+{
+    constexpr int Q = N / 8;
+    for (int x = threadIdx.x; x < kC * Q; x += kThreads) {
+        const int r = x / Q, c = (x % Q) * 8;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * ph(N) + c);
+        const bool in = r < valid;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(in ? src + r * stride + c : src),
+                     "r"(in ? 16 : 0)
+                     : "memory");
+    }
+}
+// ROWS rows of N floats of a dense array
+template <int ROWS, int N> __device__ __forceinline__ void load_f(float *dst, const float *src, int pitch)
+{
+    constexpr int Q = N / 4;
+    for (int x = threadIdx.x; x < ROWS * Q; x += kThreads) {
+        const int r = x / Q, c = (x % Q) * 4;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * pitch + c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + (size_t)r * N + c) : "memory");
+    }
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void st2(float *p, float a, float b) { *reinterpret_cast<float2 *>(p) = make_float2(a, b); }
 
 struct Where {
     int64_t b, bh;
-    int h, hk, n, t0, valid;
+    int h, hk, t0, valid;
+    size_t tok;
 };
-__device__ __forceinline__ Where where(const GdrArgs &a, int NC, int64_t bh, int n)
+__device__ __forceinline__ Where where(const GdrArgs &a, int64_t bh, int n)
 {
     Where w;
     w.bh = bh;
     w.b = bh / a.Hv;
     w.h = (int)(bh % a.Hv);
     w.hk = w.h / (a.Hv / a.Hk);
-    w.n = n;
     w.t0 = n * kC;
     w.valid = a.L - w.t0 < kC ? a.L - w.t0 : kC;
+    w.tok = (size_t)w.b * a.L + w.t0;
     return w;
 }
 
-// ---- 1. per chunk and value head: the scalars, T, P, W, U
-__global__ void __launch_bounds__(kThreads) prep_kernel(const GdrArgs a, const Layout lay)
+// ---- 1. per chunk and value head: the scalars, T, W, U = T diag(b) V and P^T dO
+template <int K, int V> struct PrepSmem {
+    bf16 k[kC * ph(K)], q[kC * ph(K)], v[kC * ph(V)], o[kC * ph(V)];
+    float a[kC * kPX], t[kC * kPX], p[kC * kPX];
+    float cs[kC], b[kC], rk[kC], rq[kC];
+};
+template <int K, int V>
+__global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, const Layout lay)
 {
-    extern __shared__ float sm[];
-    const int K = a.K, V = a.V, pk = K + 1, pv = V + 1;
-    const Where w = where(a, lay.NC, blockIdx.x / lay.NC, blockIdx.x % lay.NC);
-    float *ws = static_cast<float *>(a.workspace) + lay.base(w.bh, w.n);
-    float *Ks = sm, *Qs = Ks + kC * pk, *Vs = Qs + kC * pk, *As = Vs + kC * pv, *Ts = As + kC * 65, *vec = Ts + kC * 65;
-    float *cs = vec, *bb = vec + kC, *rk = vec + 2 * kC, *rq = vec + 3 * kC;
-    const size_t tok = (size_t)w.b * a.L + w.t0;
-    load_rows(Ks, static_cast<const bf16 *>(a.k) + (tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid, K);
-    load_rows(Qs, static_cast<const bf16 *>(a.q) + (tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid, K);
-    load_rows(Vs, static_cast<const bf16 *>(a.v) + (tok * a.Hv + w.h) * V, (size_t)a.Hv * V, w.valid, V);
+    extern __shared__ __align__(16) uint8_t raw[];
+    PrepSmem<K, V> &s = *reinterpret_cast<PrepSmem<K, V> *>(raw);
+    const GdrArgs &a = g.f;
+    const int n = blockIdx.x % lay.NC;
+    const Where w = where(a, blockIdx.x / lay.NC, n);
+    float *ws = static_cast<float *>(a.workspace) + lay.base(w.bh, n);
+    load_rows<K>(s.k, static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+    load_rows<K>(s.q, static_cast<const bf16 *>(a.q) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+    load_rows<V>(s.v, static_cast<const bf16 *>(a.v) + (w.tok * a.Hv + w.h) * V, (size_t)a.Hv * V, w.valid);
+    load_rows<V>(s.o, static_cast<const bf16 *>(g.dout) + (w.tok * a.Hv + w.h) * V, (size_t)a.Hv * V, w.valid);
+    cp_commit();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) {
         const float bias = a.bias ? a.bias[w.h] : 0.f, Ah = a.A[w.h] * kLog2e;
-        float g[2];
+        float gl[2];
         for (int i = 0; i < 2; i++) {
             const int r = 2 * lane + i;
-            g[i] = 0.f;
-            bb[r] = 0.f;
+            gl[i] = 0.f;
+            s.b[r] = 0.f;
             if (r < w.valid) {
-                g[i] = gdr_dt(gdr_ld(static_cast<const bf16 *>(a.delta), (tok + r) * a.Hv + w.h), bias, a.softplus) * Ah;
-                const float be = gdr_ld(static_cast<const bf16 *>(a.beta), (tok + r) * a.Hv + w.h);
-                bb[r] = a.sigmoid ? gdr_sigmoid(be) : be;
+                gl[i] = gdr_dt(gdr_ld(static_cast<const bf16 *>(a.delta), (w.tok + r) * a.Hv + w.h), bias, a.softplus) * Ah;
+                const float be = gdr_ld(static_cast<const bf16 *>(a.beta), (w.tok + r) * a.Hv + w.h);
+                s.b[r] = a.sigmoid ? gdr_sigmoid(be) : be;
             }
         }
-        float incl = g[0] + g[1];
+        float incl = gl[0] + gl[1];
         for (int o = 1; o < 32; o <<= 1) {
             const float v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o)
                 incl += v;
         }
-        cs[2 * lane] = incl - g[1];
-        cs[2 * lane + 1] = incl;
+        s.cs[2 * lane] = incl - gl[1];
+        s.cs[2 * lane + 1] = incl;
     }
+    cp_wait<0>();
     __syncthreads();
     for (int r = warp; r < kC; r += kThreads / 32) {
         float kk = 0.f, qq = 0.f;
         for (int c = lane; c < K; c += 32) {
-            kk = fmaf(Ks[r * pk + c], Ks[r * pk + c], kk);
-            qq = fmaf(Qs[r * pk + c], Qs[r * pk + c], qq);
+            const float x = bf(&s.k[r * ph(K) + c]), y = bf(&s.q[r * ph(K) + c]);
+            kk = fmaf(x, x, kk);
+            qq = fmaf(y, y, qq);
         }
         kk = warp_sum(kk);
         qq = warp_sum(qq);
         if (lane == 0) {
-            rk[r] = a.l2norm ? rsqrtf(kk + kL2Eps) : 1.f;
-            rq[r] = a.scale * (a.l2norm ? rsqrtf(qq + kL2Eps) : 1.f);
+            s.rk[r] = a.l2norm ? rsqrtf(kk + kL2Eps) : 1.f;
+            s.rq[r] = a.scale * (a.l2norm ? rsqrtf(qq + kL2Eps) : 1.f);
         }
     }
     __syncthreads();
+    const int m0 = 32 * (warp >> 2), wn = warp & 3;
     {
-        float kk[4][4], qk[4][4];
+        float kk[2][2][4], qk[2][2][4];
         zero(kk);
         zero(qk);
-        mm(kk, K, [&](int i, int k) { return Ks[i * pk + k]; }, [&](int k, int j) { return Ks[j * pk + k]; });
-        mm(qk, K, [&](int i, int k) { return Qs[i * pk + k]; }, [&](int k, int j) { return Ks[j * pk + k]; });
-        each(kk, [&](int i, int j, float v) {
-            As[i * 65 + j] = j < i ? bb[i] * ex2_mufu(cs[i] - cs[j]) * rk[i] * rk[j] * v : 0.f;
-            Ts[i * 65 + j] = 0.f;
+        auto krow = [&](int k, int j) { return bf(&s.k[j * ph(K) + k]); };
+        mm<kExact, kExact>(kk, m0, 16 * wn, K, [&](int i, int k) { return bf(&s.k[i * ph(K) + k]); }, krow);
+        mm<kExact, kExact>(qk, m0, 16 * wn, K, [&](int i, int k) { return bf(&s.q[i * ph(K) + k]); }, krow);
+        each(kk, m0, 16 * wn, [&](int i, int j, float v) {
+            s.a[i * kPX + j] = j < i ? s.b[i] * ex2_mufu(s.cs[i] - s.cs[j]) * s.rk[i] * s.rk[j] * v : 0.f;
+            s.t[i * kPX + j] = 0.f;
         });
-        each(qk, [&](int i, int j, float v) {
-            ws[lay.P() + i * kC + j] = j <= i ? ex2_mufu(cs[i] - cs[j]) * rq[i] * rk[j] * v : 0.f;
+        each(qk, m0, 16 * wn, [&](int i, int j, float v) {
+            s.p[i * kPX + j] = j <= i ? ex2_mufu(s.cs[i] - s.cs[j]) * s.rq[i] * s.rk[j] * v : 0.f;
         });
     }
     __syncthreads();
-    // (I + A)^-1 by forward substitution, a thread per column
-    if (threadIdx.x < kC) {
-        const int j = threadIdx.x;
-        for (int i = j; i < kC; i++) {
-            float v = i == j ? 1.f : 0.f;
-            for (int k = j; k < i; k++)
-                v = fmaf(-As[i * 65 + k], Ts[k * 65 + j], v);
-            Ts[i * 65 + j] = v;
+    // T = (I + A)^-1: the 16 x 16 diagonal blocks by substitution from the
+    // right (thread = row, the block's other rows by shuffles), then the
+    // 16 x 16 blocks beside them and the 32 x 32 block below: T21 = -T22 A21 T11
+    if (warp < 2) {
+        const int i = 32 * warp + lane, il = lane & 15, c0 = i - il;
+        float d[16], x[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+            d[j] = s.a[i * kPX + c0 + j];
+            x[j] = 0.f;
         }
+#pragma unroll
+        for (int k = 15; k >= 0; k--) {
+            x[k] = k == il ? 1.f : x[k];
+#pragma unroll
+            for (int j = 0; j < k; j++)
+                x[j] = fmaf(-x[k], __shfl_sync(0xffffffffu, d[j], (lane & 16) | k), x[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j++)
+            s.t[i * kPX + c0 + j] = x[j];
+    }
+    __syncthreads();
+    auto A = [&](int r0, int c0) { return [&s, r0, c0](int i, int k) { return s.a[(r0 + i) * kPX + c0 + k]; }; };
+    auto T = [&](int r0, int c0) { return [&s, r0, c0](int i, int k) { return s.t[(r0 + i) * kPX + c0 + k]; }; };
+    if (warp < 4) {   // A21 T11 of both pairs of 16 blocks, in the place of A21
+        const int r0 = 32 * (warp >> 1) + 16, c0 = r0 - 16, n0 = 8 * (warp & 1);
+        float x[1][1][4];
+        zero(x);
+        mm<kTwo, kTwo>(x, 0, n0, 16, A(r0, c0), T(c0, c0));
+        __syncwarp();
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");   // both warps have read A21
+        each(x, 0, n0, [&](int i, int j, float v) { s.a[(r0 + i) * kPX + c0 + j] = v; });
+    }
+    __syncthreads();
+    if (warp < 4) {
+        const int r0 = 32 * (warp >> 1) + 16, c0 = r0 - 16, n0 = 8 * (warp & 1);
+        float x[1][1][4];
+        zero(x);
+        mm<kTwo, kTwo>(x, 0, n0, 16, T(r0, r0), A(r0, c0));
+        each(x, 0, n0, [&](int i, int j, float v) { s.t[(r0 + i) * kPX + c0 + j] = -v; });
+    }
+    __syncthreads();
+    {   // 32 x 32: warps 2 (rows) x 4 (columns of 8)
+        float x[1][1][4];
+        zero(x);
+        mm<kTwo, kTwo>(x, m0 / 2, 8 * wn, 32, A(32, 0), T(0, 0));
+        __syncthreads();
+        each(x, m0 / 2, 8 * wn, [&](int i, int j, float v) { s.a[(32 + i) * kPX + j] = v; });
+        __syncthreads();
+        zero(x);
+        mm<kTwo, kTwo>(x, m0 / 2, 8 * wn, 32, T(32, 32), A(32, 0));
+        each(x, m0 / 2, 8 * wn, [&](int i, int j, float v) { s.t[(32 + i) * kPX + j] = -v; });
     }
     __syncthreads();
     for (int x = threadIdx.x; x < kC * kC; x += kThreads)
-        ws[lay.T() + x] = Ts[(x >> 6) * 65 + (x & 63)];
-    for (int x = threadIdx.x; x < 4 * kC; x += kThreads)
-        ws[x] = vec[x];
-    for (int c0 = 0; c0 < K; c0 += 64) {
-        float acc[4][4];
-        zero(acc);
-        mm(acc, kC, [&](int i, int k) { return Ts[i * 65 + k] * (bb[k] * ex2_mufu(cs[k]) * rk[k]); },
-           [&](int k, int j) { return Ks[k * pk + c0 + j]; });
-        each(acc, [&](int i, int j, float v) { ws[lay.W() + i * K + c0 + j] = v; });
+        ws[lay.T() + x] = s.t[(x >> 6) * kPX + (x & 63)];
+    if (threadIdx.x < kC) {
+        const int i = threadIdx.x;
+        ws[lay.cs() + i] = s.cs[i];
+        ws[lay.cs() + kC + i] = s.b[i];
+        ws[lay.rk() + i] = s.rk[i];
+        ws[lay.rq() + i] = s.rq[i];
     }
-    for (int c0 = 0; c0 < V; c0 += 64) {
-        float acc[4][4];
+    {
+        float acc[2][K / 32][4];
         zero(acc);
-        mm(acc, kC, [&](int i, int k) { return Ts[i * 65 + k] * bb[k]; }, [&](int k, int j) { return Vs[k * pv + c0 + j]; });
-        each(acc, [&](int i, int j, float v) { ws[lay.U() + i * V + c0 + j] = v; });
+        mm<kTwo, kExact>(acc, m0, K / 4 * wn, kC,
+                         [&](int i, int k) { return s.t[i * kPX + k] * (s.b[k] * ex2_mufu(s.cs[k]) * s.rk[k]); },
+                         [&](int k, int j) { return bf(&s.k[k * ph(K) + j]); });
+        pairs(acc, m0, K / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.W() + i * K + j, x, y); });
     }
+    float acc[2][V / 32][4];
+    zero(acc);
+    mm<kTwo, kExact>(acc, m0, V / 4 * wn, kC, [&](int i, int k) { return s.t[i * kPX + k] * s.b[k]; },
+                     [&](int k, int j) { return bf(&s.v[k * ph(V) + j]); });
+    pairs(acc, m0, V / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.U() + i * V + j, x, y); });
+    zero(acc);
+    mm<kTwo, kExact>(acc, m0, V / 4 * wn, kC, [&](int i, int k) { return s.p[k * kPX + i]; },
+                     [&](int k, int j) { return bf(&s.o[k * ph(V) + j]); });
+    pairs(acc, m0, V / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.dN() + i * V + j, x, y); });
 }
 
-// ---- 2. forward over the chunks, 32 state rows per block: S0 and N
-template <int K> __global__ void __launch_bounds__(kThreads) chain_kernel(const GdrArgs a, const Layout lay)
+// ---- 2. forward over the chunks, 32 state rows per block: S0, and N in U's place
+template <int K> struct ChainSmem {
+    float w[2][kC * pf(K)];
+    bf16 k[2][kC * ph(K)];
+    float s[kSlice * pf(K)], n[kC * (kSlice + 8)];
+};
+template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const GdrArgs a, const Layout lay)
 {
-    extern __shared__ float sm[];
-    constexpr int pk = K + 1, ps = kSlice + 1;
-    const int slices = a.V / kSlice;
+    extern __shared__ __align__(16) uint8_t raw[];
+    ChainSmem<K> &s = *reinterpret_cast<ChainSmem<K> *>(raw);
+    constexpr int pn = kSlice + 8;
+    const int slices = a.V / kSlice, warp = threadIdx.x >> 5;
     const int64_t bh = blockIdx.x / slices;
     const int v0 = (blockIdx.x % slices) * kSlice;
-    float *Ws = sm, *Ke = Ws + kC * pk, *Ss = Ke + kC * pk, *Ns = Ss + kSlice * pk;
+    float *base = static_cast<float *>(a.workspace);
+    auto fetch = [&](int n) {
+        if (n < lay.NC) {
+            const Where w = where(a, bh, n);
+            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pf(K));
+            load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+        }
+        cp_commit();
+    };
+    fetch(0);
     for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-        Ss[(x / K) * pk + x % K] = a.init ? a.init[((size_t)bh * a.V + v0) * K + x] : 0.f;
+        s.s[(x / K) * pf(K) + x % K] = a.init ? a.init[((size_t)bh * a.V + v0) * K + x] : 0.f;
+    const int mN = 16 * (warp >> 1), nN = 16 * (warp & 1);   // N: 64 x 32 as 4 x 2 warps
+    constexpr int NT = K / 64;                               // the state: 32 x K as 1 x 8
     for (int n = 0; n < lay.NC; n++) {
-        const Where w = where(a, lay.NC, bh, n);
-        float *ws = static_cast<float *>(a.workspace) + lay.base(bh, n);
-        __syncthreads();
-        load_f(Ws, ws + lay.W(), kC, K, pk, K);
-        load_rows(Ke, static_cast<const bf16 *>(a.k) + (((size_t)w.b * a.L + w.t0) * a.Hk + w.hk) * K,
-                  (size_t)a.Hk * K, w.valid, K);
-        for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-            ws[lay.S0() + (size_t)v0 * K + x] = Ss[(x / K) * pk + x % K];
-        __syncthreads();
-        const float end = ws[lay.cs() + kC - 1];
-        float acc[4][2];
-        zero(acc);
-        mm(acc, K, [&](int i, int k) { return Ws[i * pk + k]; }, [&](int k, int j) { return Ss[j * pk + k]; });
-        each(acc, [&](int i, int j, float v) {
-            const float x = ws[lay.U() + i * a.V + v0 + j] - v;
-            ws[lay.N() + i * a.V + v0 + j] = x;
-            Ns[i * ps + j] = x * ws[lay.rk() + i] * ex2_mufu(end - ws[lay.cs() + i]);
+        float *ws = base + lay.base(bh, n);
+        fetch(n + 1);
+        float u[1][2][4];   // this thread's part of U, and the factors of its rows of N
+        pairs(u, mN, nN, [&](int i, int j, float &x, float &y) {
+            const float2 f = *reinterpret_cast<const float2 *>(ws + lay.U() + i * a.V + v0 + j);
+            x = f.x, y = f.y;
         });
-        __syncthreads();
-        float up[2][K / 16];
-        zero(up);
-        mm(up, kC, [&](int i, int k) { return Ns[k * ps + i]; }, [&](int k, int j) { return Ke[k * pk + j]; });
-        const float dec = ex2_mufu(end);
-        each(up, [&](int i, int j, float v) { Ss[i * pk + j] = fmaf(dec, Ss[i * pk + j], v); });
-    }
-}
-
-// ---- 3. in reverse: dS1 and dN
-template <int K> __global__ void __launch_bounds__(kThreads) reverse_kernel(const GdrBwdArgs g, const Layout lay)
-{
-    extern __shared__ float sm[];
-    const GdrArgs &a = g.f;
-    constexpr int pk = K + 1, ps = kSlice + 1;
-    const int slices = a.V / kSlice;
-    const int64_t bh = blockIdx.x / slices;
-    const int v0 = (blockIdx.x % slices) * kSlice;
-    float *Ws = sm, *Ks = Ws + kC * pk, *Qs = Ks + kC * pk, *Gs = Qs + kC * pk, *Ns = Gs + kSlice * pk,
-          *Os = Ns + kC * ps, *Ps = Os + kC * ps;
-    for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-        Gs[(x / K) * pk + x % K] = g.dlast ? g.dlast[((size_t)bh * a.V + v0) * K + x] : 0.f;
-    for (int n = lay.NC - 1; n >= 0; n--) {
-        const Where w = where(a, lay.NC, bh, n);
-        float *ws = static_cast<float *>(a.workspace) + lay.base(bh, n);
-        const size_t tok = (size_t)w.b * a.L + w.t0;
-        __syncthreads();
-        load_f(Ws, ws + lay.W(), kC, K, pk, K);
-        load_f(Ps, ws + lay.P(), kC, kC, 65, kC);
-        load_rows(Ks, static_cast<const bf16 *>(a.k) + (tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid, K);
-        load_rows(Qs, static_cast<const bf16 *>(a.q) + (tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid, K);
-        load_rows(Os, static_cast<const bf16 *>(g.dout) + (tok * a.Hv + w.h) * a.V + v0, (size_t)a.Hv * a.V, w.valid,
-                  kSlice);
-        for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-            ws[lay.dS() + (size_t)v0 * K + x] = Gs[(x / K) * pk + x % K];
-        __syncthreads();
         const float end = ws[lay.cs() + kC - 1];
-        float acc[4][2];
-        zero(acc);
-        mm(acc, K, [&](int i, int k) { return Ks[i * pk + k]; }, [&](int k, int j) { return Gs[j * pk + k]; });
-        each(acc, [&](int i, int, float &v) { v *= ws[lay.rk() + i] * ex2_mufu(end - ws[lay.cs() + i]); });
-        mm(acc, kC, [&](int i, int k) { return Ps[k * 65 + i]; }, [&](int k, int j) { return Os[k * ps + j]; });
-        each(acc, [&](int i, int j, float v) {
-            ws[lay.dN() + i * a.V + v0 + j] = v;
-            Ns[i * ps + j] = -v;
-        });
+        cp_wait<1>();
         __syncthreads();
-        for (int x = threadIdx.x; x < kC * kSlice; x += kThreads) {
-            const int i = x / kSlice;
-            Os[i * ps + x % kSlice] *= ws[lay.rq() + i] * ex2_mufu(ws[lay.cs() + i]);
+        for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
+            *reinterpret_cast<float4 *>(ws + lay.S0() + (size_t)v0 * K + x) =
+                *reinterpret_cast<const float4 *>(&s.s[(x / K) * pf(K) + x % K]);
+        const float *W = s.w[n & 1];
+        const bf16 *Kt = s.k[n & 1];
+        float acc[1][2][4];
+        zero(acc);
+        mm<kTwo, kTwo>(acc, mN, nN, K, [&](int i, int k) { return W[i * pf(K) + k]; },
+                       [&](int k, int j) { return s.s[j * pf(K) + k]; });
+        {
+            const int i0 = mN + ((threadIdx.x & 31) >> 2);
+            const float e[2] = {ws[lay.rk() + i0] * ex2_mufu(end - ws[lay.cs() + i0]),
+                                ws[lay.rk() + i0 + 8] * ex2_mufu(end - ws[lay.cs() + i0 + 8])};
+#pragma unroll
+            for (int q = 0; q < 2; q++)
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+                    acc[0][q][x] = u[0][q][x] - acc[0][q][x];
+            pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
+                st2(ws + lay.U() + i * a.V + v0 + j, x, y);
+                const float f = e[(i - i0) >> 3];
+                st2(&s.n[i * pn + j], x * f, y * f);
+            });
         }
         __syncthreads();
-        float up[2][K / 16];
+        float up[2][NT][4];
         zero(up);
-        mm(up, kC, [&](int i, int k) { return Ns[k * ps + i]; }, [&](int k, int j) { return Ws[k * pk + j]; });
-        mm(up, kC, [&](int i, int k) { return Os[k * ps + i]; }, [&](int k, int j) { return Qs[k * pk + j]; });
+        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, [&](int i, int k) { return s.n[k * pn + i]; },
+                         [&](int k, int j) { return bf(&Kt[k * ph(K) + j]); });
         const float dec = ex2_mufu(end);
-        each(up, [&](int i, int j, float v) { Gs[i * pk + j] = fmaf(dec, Gs[i * pk + j], v); });
+        each(up, 0, 8 * NT * warp, [&](int i, int j, float v) {
+            float *p = &s.s[i * pf(K) + j];
+            *p = fmaf(dec, *p, v);
+        });
+        __syncthreads();
     }
-    __syncthreads();
-    if (g.dinit)
+}
+
+// ---- 3. in reverse: dS1, and dN in the place of P^T dO
+template <int K> struct ReverseSmem {
+    float w[2][kC * pf(K)];
+    bf16 k[2][kC * ph(K)], q[2][kC * ph(K)], o[2][kC * ph(kSlice)];
+    float g[kSlice * pf(K)], n[kC * (kSlice + 8)];
+    float f[kC];
+};
+template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(const GdrBwdArgs ga, const Layout lay)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    ReverseSmem<K> &s = *reinterpret_cast<ReverseSmem<K> *>(raw);
+    const GdrArgs &a = ga.f;
+    constexpr int pn = kSlice + 8;
+    const int slices = a.V / kSlice, warp = threadIdx.x >> 5;
+    const int64_t bh = blockIdx.x / slices;
+    const int v0 = (blockIdx.x % slices) * kSlice;
+    float *base = static_cast<float *>(a.workspace);
+    auto fetch = [&](int n) {
+        if (n >= 0) {
+            const Where w = where(a, bh, n);
+            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pf(K));
+            load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+            load_rows<K>(s.q[n & 1], static_cast<const bf16 *>(a.q) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+            load_rows<kSlice>(s.o[n & 1], static_cast<const bf16 *>(ga.dout) + (w.tok * a.Hv + w.h) * a.V + v0,
+                              (size_t)a.Hv * a.V, w.valid);
+        }
+        cp_commit();
+    };
+    fetch(lay.NC - 1);
+    for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
+        s.g[(x / K) * pf(K) + x % K] = ga.dlast ? ga.dlast[((size_t)bh * a.V + v0) * K + x] : 0.f;
+    const int mN = 16 * (warp >> 1), nN = 16 * (warp & 1);
+    constexpr int NT = K / 64;
+    for (int n = lay.NC - 1; n >= 0; n--) {
+        float *ws = base + lay.base(bh, n);
+        fetch(n - 1);
+        float u[1][2][4];
+        pairs(u, mN, nN, [&](int i, int j, float &x, float &y) {
+            const float2 f = *reinterpret_cast<const float2 *>(ws + lay.dN() + i * a.V + v0 + j);
+            x = f.x, y = f.y;
+        });
+        const float end = ws[lay.cs() + kC - 1];
+        if (threadIdx.x < kC)
+            s.f[threadIdx.x] = ws[lay.rq() + threadIdx.x] * ex2_mufu(ws[lay.cs() + threadIdx.x]);
+        cp_wait<1>();
+        __syncthreads();
+        for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
+            *reinterpret_cast<float4 *>(ws + lay.dS() + (size_t)v0 * K + x) =
+                *reinterpret_cast<const float4 *>(&s.g[(x / K) * pf(K) + x % K]);
+        const float *W = s.w[n & 1];
+        const bf16 *Kt = s.k[n & 1], *Qt = s.q[n & 1], *Ot = s.o[n & 1];
+        float acc[1][2][4];
+        zero(acc);
+        mm<kExact, kTwo>(acc, mN, nN, K, [&](int i, int k) { return bf(&Kt[i * ph(K) + k]); },
+                         [&](int k, int j) { return s.g[j * pf(K) + k]; });
+        {
+            const int i0 = mN + ((threadIdx.x & 31) >> 2);
+            const float e[2] = {ws[lay.rk() + i0] * ex2_mufu(end - ws[lay.cs() + i0]),
+                                ws[lay.rk() + i0 + 8] * ex2_mufu(end - ws[lay.cs() + i0 + 8])};
+#pragma unroll
+            for (int q = 0; q < 2; q++)
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+                    acc[0][q][x] = fmaf(e[x >> 1], acc[0][q][x], u[0][q][x]);
+            pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
+                st2(ws + lay.dN() + i * a.V + v0 + j, x, y);
+                st2(&s.n[i * pn + j], -x, -y);
+            });
+        }
+        __syncthreads();
+        float up[2][NT][4];
+        zero(up);
+        mm<kTwo, kTwo>(up, 0, 8 * NT * warp, kC, [&](int i, int k) { return s.n[k * pn + i]; },
+                       [&](int k, int j) { return W[k * pf(K) + j]; });
+        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, [&](int i, int k) { return s.f[k] * bf(&Ot[k * ph(kSlice) + i]); },
+                         [&](int k, int j) { return bf(&Qt[k * ph(K) + j]); });
+        const float dec = ex2_mufu(end);
+        each(up, 0, 8 * NT * warp, [&](int i, int j, float v) {
+            float *p = &s.g[i * pf(K) + j];
+            *p = fmaf(dec, *p, v);
+        });
+        __syncthreads();
+    }
+    if (ga.dinit)
         for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-            g.dinit[((size_t)bh * a.V + v0) * K + x] = Gs[(x / K) * pk + x % K];
+            ga.dinit[((size_t)bh * a.V + v0) * K + x] = s.g[(x / K) * pf(K) + x % K];
 }
 
 // ---- 4. per chunk and key head: every gradient
+template <int K, int V> struct GradSmem {
+    bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(V)];
+    float n[kC * pf(V)], r[kC * pf(V)], x[kC * kPX];
+    float m[kC * pf(K)];   // T first, then 64 rows of a state at a time
+    float cs[4 * kC];       // cs, b, rk, rq as in the workspace
+    float dcs[kC], sum[6][4][kC], red[8];   // sum: row sums of each column of warps
+};
 template <int K, int V>
-__global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs g, const Layout lay, float *parts)
+__global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, const Layout lay, float *partial)
 {
-    extern __shared__ float sm[];
-    const GdrArgs &a = g.f;
-    constexpr int pk = K + 1, pv = V + 1, RK = K / 16, RV = V / 16;
-    const int per_k = a.Hv / a.Hk;
+    extern __shared__ __align__(16) uint8_t raw[];
+    GradSmem<K, V> &s = *reinterpret_cast<GradSmem<K, V> *>(raw);
+    const GdrArgs &a = ga.f;
+    constexpr int NK = K / 32, NV = V / 32;
+    const int per_k = a.Hv / a.Hk, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t bhk = blockIdx.x / lay.NC;
     const int n = blockIdx.x % lay.NC;
     const int64_t b = bhk / a.Hk;
     const int hk = (int)(bhk % a.Hk);
-    float *Ks = sm, *Qs = Ks + kC * pk, *Ns = Qs + kC * pk, *Rs = Ns + kC * pv, *Os = Rs + kC * pv, *Xs = Os + kC * pv,
-          *vec = Xs + kC * 65;
-    float *cs = vec, *bb = vec + kC, *rk = vec + 2 * kC, *rq = vec + 3 * kC, *dcs = vec + 4 * kC, *db = vec + 5 * kC,
-          *sv = vec + 6 * kC, *zv = vec + 7 * kC, *red = vec + 8 * kC;   // red: one value per warp
+    const float *cs = s.cs, *bb = s.cs + kC, *rk = s.cs + 2 * kC, *rq = s.cs + 3 * kC;
     const int t0 = n * kC, valid = a.L - t0 < kC ? a.L - t0 : kC;
     const size_t tok = (size_t)b * a.L + t0;
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const bf16 *kp = static_cast<const bf16 *>(a.k) + (tok * a.Hk + hk) * K;
-    const bf16 *qp = static_cast<const bf16 *>(a.q) + (tok * a.Hk + hk) * K;
-    float dK[4][RK], dQ[4][RK];
+    const int m0 = 32 * (warp >> 2), wn = warp & 3, gq = lane >> 2, tq = lane & 3;
+    const int nK = K / 4 * wn, nV = V / 4 * wn, nC = 16 * wn;   // this warp's columns
+    load_rows<K>(s.k, static_cast<const bf16 *>(a.k) + (tok * a.Hk + hk) * K, (size_t)a.Hk * K, valid);
+    load_rows<K>(s.q, static_cast<const bf16 *>(a.q) + (tok * a.Hk + hk) * K, (size_t)a.Hk * K, valid);
+    auto Kt = [&](int i, int k) { return bf(&s.k[i * ph(K) + k]); };
+    auto Qt = [&](int i, int k) { return bf(&s.q[i * ph(K) + k]); };
+    float dK[2][NK][4], dQ[2][NK][4];   // of the unit rows (scale q^ for q), all value heads
     zero(dK);
     zero(dQ);
-    // sums over a row's 16 threads of this row layout (lanes of a half warp)
-    auto row_add = [&](float v) {
+    // this thread's rows: m0 + 16 m + gq + 8 h
+    auto row_of = [&](int x) { return m0 + 16 * (x >> 1) + gq + 8 * (x & 1); };
+    // rows' sums over the warp's columns, from each thread's part, to sum[which]
+    auto put_rows = [&](int which, const float (&v)[4]) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
+        for (int x = 0; x < 4; x++) {
+            float r = v[x];
+            r += __shfl_xor_sync(0xffffffffu, r, 1);
+            r += __shfl_xor_sync(0xffffffffu, r, 2);
+            if (tq == 0)
+                s.sum[which][wn][row_of(x)] = r;
+        }
+    };
+    auto all = [&](int which, int row) {
+        return (s.sum[which][0][row] + s.sum[which][1][row]) + (s.sum[which][2][row] + s.sum[which][3][row]);
     };
     for (int hh = 0; hh < per_k; hh++) {
         const int h = hk * per_k + hh;
@@ -363,147 +611,197 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs g, c
         const float *S0 = ws + lay.S0(), *dS = ws + lay.dS();
         const bf16 *vp = static_cast<const bf16 *>(a.v) + (tok * a.Hv + h) * V;
         __syncthreads();
-        for (int x = threadIdx.x; x < 4 * kC; x += kThreads)
-            vec[x] = ws[x];
-        load_rows(Ks, kp, (size_t)a.Hk * K, valid, K);
-        load_rows(Qs, qp, (size_t)a.Hk * K, valid, K);
-        load_rows(Os, static_cast<const bf16 *>(g.dout) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid, V);
-        load_f(Ns, ws + lay.N(), kC, V, pv, V);
-        load_f(Rs, ws + lay.dN(), kC, V, pv, V);
-        load_f(Xs, ws + lay.T(), kC, kC, 65, kC);
+        s.cs[threadIdx.x] = ws[threadIdx.x];
+        load_rows<V>(s.o, static_cast<const bf16 *>(ga.dout) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid);
+        load_f<kC, V>(s.n, ws + lay.U(), pf(V));
+        load_f<kC, V>(s.r, ws + lay.dN(), pf(V));
+        load_f<kC, kC>(s.m, ws + lay.T(), kPX);
+        cp_commit();
+        cp_wait<0>();
         __syncthreads();
-        for (int x = threadIdx.x; x < kC * K; x += kThreads) {
-            const int r = x / K, c = x % K;
-            Ks[r * pk + c] *= rk[r];
-            Qs[r * pk + c] *= rq[r];
-        }
         const float end = cs[kC - 1];
         // R' = T^T dN
-        float r[4][RV];
-        zero(r);
-        mm(r, kC, [&](int i, int k) { return Xs[k * 65 + i]; }, [&](int k, int j) { return Rs[k * pv + j]; });
-        __syncthreads();
-        each(r, [&](int i, int j, float v) { Rs[i * pv + j] = v; });
-        float dbr[4] = {};
-        each(r, [&](int i, int j, float v) {
-            if (i < valid) {
-                static_cast<bf16 *>(g.dv)[((tok + i) * a.Hv + h) * V + j] = __float2bfloat16_rn(bb[i] * v);
-                dbr[(i - ty) >> 4] = fmaf(v, __bfloat162float(vp[(size_t)i * a.Hv * V + j]), dbr[(i - ty) >> 4]);
-            }
-        });
-        __syncthreads();
-        // (dA o G) and (dP o G)
-        float xa[4][4], xp[4][4];
-        zero(xa);
-        zero(xp);
-        mm(xa, V, [&](int i, int k) { return Rs[i * pv + k]; }, [&](int k, int j) { return Ns[j * pv + k]; });
-        mm(xp, V, [&](int i, int k) { return Os[i * pv + k]; }, [&](int k, int j) { return Ns[j * pv + k]; });
-        each(xa, [&](int i, int j, float &v) { v = j < i ? -v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
-        each(xp, [&](int i, int j, float &v) { v = j <= i ? v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
-        __syncthreads();
-        // E = dP o P + dA o A below the diagonal, then its sums along rows up
-        // to each column (thread i: row i)
         {
-            float kk[4][4], qk[4][4];
+            float r[2][NV][4];
+            zero(r);
+            mm<kTwo, kTwo>(r, m0, nV, kC, [&](int i, int k) { return s.m[k * kPX + i]; },
+                           [&](int k, int j) { return s.r[k * pf(V) + j]; });
+            __syncthreads();
+            float dbr[4] = {};
+#pragma unroll
+            for (int m = 0; m < 2; m++)
+#pragma unroll
+                for (int q = 0; q < NV; q++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const int i = m0 + 16 * m + gq + 8 * e, j = nV + 8 * q + 2 * tq;
+                        const float x = r[m][q][2 * e], y = r[m][q][2 * e + 1];
+                        st2(&s.r[i * pf(V) + j], x, y);
+                        if (i < valid) {
+                            const __nv_bfloat162 vv = *reinterpret_cast<const __nv_bfloat162 *>(vp + (size_t)i * a.Hv * V + j);
+                            dbr[2 * m + e] = fmaf(x, __low2float(vv), fmaf(y, __high2float(vv), dbr[2 * m + e]));
+                            *reinterpret_cast<__nv_bfloat162 *>(static_cast<bf16 *>(ga.dv) + ((tok + i) * a.Hv + h) * V + j) =
+                                __floats2bfloat162_rn(bb[i] * x, bb[i] * y);
+                        }
+                    }
+            put_rows(0, dbr);
+        }
+        __syncthreads();
+        // dA o G and dP o G, and with them E
+        float xp[2][2][4], xa[2][2][4];
+        {
+            zero(xa);
+            zero(xp);
+            auto Nt = [&](int k, int j) { return s.n[j * pf(V) + k]; };
+            mm<kTwo, kTwo>(xa, m0, nC, V, [&](int i, int k) { return s.r[i * pf(V) + k]; }, Nt);
+            mm<kExact, kTwo>(xp, m0, nC, V, [&](int i, int k) { return bf(&s.o[i * ph(V) + k]); }, Nt);
+            each(xa, m0, nC, [&](int i, int j, float &v) { v = j < i ? -v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
+            each(xp, m0, nC, [&](int i, int j, float &v) { v = j <= i ? v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
+            float kk[2][2][4], qk[2][2][4];
             zero(kk);
             zero(qk);
-            mm(kk, K, [&](int i, int k) { return Ks[i * pk + k]; }, [&](int k, int j) { return Ks[j * pk + k]; });
-            mm(qk, K, [&](int i, int k) { return Qs[i * pk + k]; }, [&](int k, int j) { return Ks[j * pk + k]; });
+            auto krow = [&](int k, int j) { return Kt(j, k); };
+            mm<kExact, kExact>(kk, m0, nC, K, Kt, krow);
+            mm<kExact, kExact>(qk, m0, nC, K, Qt, krow);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int m = 0; m < 2; m++)
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int row = ty + 16 * i, col = tx + 16 * j;
-                    Xs[row * 65 + col] =
-                        col < row ? fmaf(xp[i][j], qk[i][j], bb[row] * xa[i][j] * kk[i][j]) : 0.f;
-                }
+                for (int q = 0; q < 2; q++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int i = m0 + 16 * m + gq + 8 * (e >> 1), j = nC + 8 * q + 2 * tq + (e & 1);
+                        const float pa = bb[i] * rk[i] * xa[m][q][e] * kk[m][q][e];
+                        s.x[i * kPX + j] = j < i ? rk[j] * fmaf(rq[i] * xp[m][q][e], qk[m][q][e], pa) : 0.f;
+                    }
         }
         __syncthreads();
-        if (threadIdx.x < kC) {
-            float run = 0.f;
-            for (int j = 0; j < kC; j++) {
-                const float e = Xs[threadIdx.x * 65 + j];
-                Xs[threadIdx.x * 65 + j] = run;   // the sum of columns < j
-                run += e;
+        // sums of E over i >= t > j: along each row first (four threads a row), then down
+        {
+            const int i = threadIdx.x >> 2, part = threadIdx.x & 3;
+            float v[16], run = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                v[j] = run;   // the sum of this part's columns before j
+                run += s.x[i * kPX + 16 * part + j];
             }
+            float before = run;   // of the parts to the left
+            const float u1 = __shfl_up_sync(0xffffffffu, run, 1), u2 = __shfl_up_sync(0xffffffffu, run, 2),
+                        u3 = __shfl_up_sync(0xffffffffu, run, 3);
+            before = (part > 2 ? u3 : 0.f) + (part > 1 ? u2 : 0.f) + (part > 0 ? u1 : 0.f);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; j++)
+                s.x[i * kPX + 16 * part + j] = before + v[j];
         }
         __syncthreads();
-        if (threadIdx.x < kC) {
+        {
+            const int t = threadIdx.x >> 2, part = threadIdx.x & 3;
             float d = 0.f;
-            for (int i = threadIdx.x; i < kC; i++)
-                d += Xs[i * 65 + threadIdx.x];
-            dcs[threadIdx.x] = d;
+            for (int i = t + part; i < kC; i += 4)
+                d += s.x[i * kPX + t];
+            d += __shfl_xor_sync(0xffffffffu, d, 1);
+            d += __shfl_xor_sync(0xffffffffu, d, 2);
+            if (part == 0)
+                s.dcs[t] = d;
         }
         __syncthreads();
-        each(xa, [&](int i, int j, float v) { Xs[i * 65 + j] = v; });
-        __syncthreads();
-        float Y[4][RK], Z[4][RK], q[4][RK], ss[4], zz[4];
+        each(xa, m0, nC, [&](int i, int j, float v) { s.x[i * kPX + j] = v; });
+        // Y = -c R' S0 and q = c dO S0, 64 rows of S0 at a time
+        float Y[2][NK][4], q[2][NK][4];
         zero(Y);
-        zero(Z);
         zero(q);
-        // sum over the row's threads of k^ or q~ times a row of products
-        auto row_dot = [&](const float *M, const float (&m)[RK], int row) {
-            float v = 0.f;
+        for (int v0 = 0; v0 < V; v0 += 64) {
+            __syncthreads();
+            load_f<kC, K>(s.m, S0 + (size_t)v0 * K, pf(K));
+            cp_commit();
+            cp_wait<0>();
+            __syncthreads();
+            auto St = [&](int k, int j) { return s.m[k * pf(K) + j]; };
+            mm<kTwo, kTwo>(Y, m0, nK, 64, [&](int i, int k) { return s.r[i * pf(V) + v0 + k]; }, St);
+            mm<kExact, kTwo>(q, m0, nK, 64, [&](int i, int k) { return bf(&s.o[i * ph(V) + v0 + k]); }, St);
+        }
+        {
+            each(Y, m0, nK, [&](int i, int, float &v) { v *= -ex2_mufu(cs[i]); });
+            each(q, m0, nK, [&](int i, int, float &v) { v *= ex2_mufu(cs[i]); });
+            float ky[4] = {}, qq[4] = {};
+            dots(Y, m0, nK, Kt, ky);
+            dots(q, m0, nK, Qt, qq);
 #pragma unroll
-            for (int j = 0; j < RK; j++)
-                v = fmaf(M[row * pk + tx + 16 * j], m[j], v);
-            return row_add(v);
-        };
-        // Y = (dA o G) K^ - c R' S0
-        mm(Y, V, [&](int i, int k) { return Rs[i * pv + k]; }, [&](int k, int j) { return S0[(size_t)k * K + j]; });
-        each(Y, [&](int i, int, float &v) { v *= -ex2_mufu(cs[i]); });
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            ss[i] = bb[ty + 16 * i] * row_dot(Ks, Y[i], ty + 16 * i);
-        mm(Y, kC, [&](int i, int k) { return Xs[i * 65 + k]; }, [&](int k, int j) { return Ks[k * pk + j]; });
-        // Z = e N dS1 + (dA o b G)^T K^ + (dP o G)^T Q~
-        mm(Z, V, [&](int i, int k) { return Ns[i * pv + k]; }, [&](int k, int j) { return dS[(size_t)k * K + j]; });
-        each(Z, [&](int i, int, float &v) { v *= ex2_mufu(end - cs[i]); });
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            zz[i] = row_dot(Ks, Z[i], ty + 16 * i);
-        mm(Z, kC, [&](int i, int k) { return bb[k] * Xs[k * 65 + i]; }, [&](int k, int j) { return Ks[k * pk + j]; });
-        __syncthreads();
-        each(xp, [&](int i, int j, float v) { Xs[i * 65 + j] = v; });
-        __syncthreads();
-        mm(Z, kC, [&](int i, int k) { return Xs[k * 65 + i]; }, [&](int k, int j) { return Qs[k * pk + j]; });
-        mm(q, V, [&](int i, int k) { return Os[i * pv + k]; }, [&](int k, int j) { return S0[(size_t)k * K + j]; });
-        each(q, [&](int i, int, float &v) { v *= ex2_mufu(cs[i]); });
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            ss[i] += row_dot(Qs, q[i], ty + 16 * i);
-        mm(q, kC, [&](int i, int k) { return Xs[i * 65 + k]; }, [&](int k, int j) { return Ks[k * pk + j]; });
-        // c_end <dS1, S0>
-        const float dec = ex2_mufu(end);
-        float through = 0.f;
-        for (int x = threadIdx.x; x < V * K; x += kThreads)
-            through = fmaf(dec * dS[x], S0[x], through);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int row = ty + 16 * i;
-#pragma unroll
-            for (int j = 0; j < RK; j++) {
-                dK[i][j] += fmaf(bb[row], Y[i][j], Z[i][j]);
-                dQ[i][j] += q[i][j];
+            for (int x = 0; x < 4; x++) {
+                const int i = row_of(x);
+                qq[x] = fmaf(rq[i], qq[x], bb[i] * rk[i] * ky[x]);
             }
-            const float ky = row_dot(Ks, Y[i], row), dbv = row_add(dbr[i]);
-            if (tx == 0) {
-                sv[row] = ss[i];
-                zv[row] = zz[i];
-                db[row] = dbv + ky;
+            put_rows(1, qq);   // s
+        }
+        // the rest of Y, and of q: one part is enough for their bf16 results
+        mm<kOne, kExact>(Y, m0, nK, kC, [&](int i, int k) { return s.x[i * kPX + k] * rk[k]; }, Kt);
+        {
+            float ky[4] = {};
+            dots(Y, m0, nK, Kt, ky);
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                ky[x] *= rk[row_of(x)];
+            put_rows(2, ky);
+            each(Y, m0, nK, [&](int i, int, float &v) { v *= bb[i]; });
+#pragma unroll
+            for (int m = 0; m < 2; m++)
+#pragma unroll
+                for (int p = 0; p < NK; p++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        dK[m][p][e] += Y[m][p][e];
+        }
+        // Z = e N dS1 + ..., in Y's registers
+        zero(Y);
+        float through = 0.f;
+        const float dec = ex2_mufu(end);
+        for (int v0 = 0; v0 < V; v0 += 64) {
+            __syncthreads();
+            load_f<kC, K>(s.m, dS + (size_t)v0 * K, pf(K));
+            cp_commit();
+            cp_wait<0>();
+            __syncthreads();
+            mm<kTwo, kTwo>(Y, m0, nK, 64, [&](int i, int k) { return s.n[i * pf(V) + v0 + k]; },
+                           [&](int k, int j) { return s.m[k * pf(K) + j]; });
+            for (int x = threadIdx.x * 4; x < 64 * K; x += kThreads * 4) {   // c_end <dS1, S0>
+                const float4 f = *reinterpret_cast<const float4 *>(S0 + (size_t)v0 * K + x);
+                const float4 d = *reinterpret_cast<const float4 *>(&s.m[(x / K) * pf(K) + x % K]);
+                through = fmaf(dec * d.x, f.x, fmaf(dec * d.y, f.y, fmaf(dec * d.z, f.z, fmaf(dec * d.w, f.w, through))));
             }
         }
-        through = warp_sum(through);
-        if ((threadIdx.x & 31) == 0)
-            red[threadIdx.x >> 5] = through;
+        each(Y, m0, nK, [&](int i, int, float &v) { v *= ex2_mufu(end - cs[i]); });
+        {
+            float kz[4] = {};
+            dots(Y, m0, nK, Kt, kz);
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                kz[x] *= rk[row_of(x)];
+            put_rows(3, kz);   // z
+        }
+        mm<kOne, kExact>(Y, m0, nK, kC, [&](int i, int k) { return s.x[k * kPX + i] * (bb[k] * rk[k]); }, Kt);
         __syncthreads();
-        if (threadIdx.x < 32) {
-            const int lane = threadIdx.x;
-            float all = 0.f;
-            for (int k = 0; k < kThreads / 32; k++)
-                all += red[k];
+        each(xp, m0, nC, [&](int i, int j, float v) { s.x[i * kPX + j] = v; });
+        through = warp_sum(through);
+        if (lane == 0)
+            s.red[warp] = through;
+        __syncthreads();
+        mm<kOne, kExact>(Y, m0, nK, kC, [&](int i, int k) { return s.x[k * kPX + i] * rq[k]; }, Qt);
+        mm<kOne, kExact>(q, m0, nK, kC, [&](int i, int k) { return s.x[i * kPX + k] * rk[k]; }, Kt);
+#pragma unroll
+        for (int m = 0; m < 2; m++)
+#pragma unroll
+            for (int p = 0; p < NK; p++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    dK[m][p][e] += Y[m][p][e];
+                    dQ[m][p][e] += q[m][p][e];
+                }
+        if (warp == 0) {
+            float thr = 0.f;
+            for (int k = 0; k < 8; k++)
+                thr += s.red[k];
             // sums of s from each step on, of z before each step
-            const float s0 = sv[2 * lane], s1 = sv[2 * lane + 1], z0 = zv[2 * lane], z1 = zv[2 * lane + 1];
+            const float s0 = all(1, 2 * lane), s1 = all(1, 2 * lane + 1), z0 = all(3, 2 * lane), z1 = all(3, 2 * lane + 1);
             float down = s0 + s1, up = z0 + z1;
             for (int o = 1; o < 32; o <<= 1) {
                 const float v = __shfl_down_sync(0xffffffffu, down, o), u = __shfl_up_sync(0xffffffffu, up, o);
@@ -514,62 +812,67 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs g, c
             }
             const float nd = __shfl_down_sync(0xffffffffu, down, 1), pu = __shfl_up_sync(0xffffffffu, up, 1);
             const float after = lane < 31 ? nd : 0.f, before = lane > 0 ? pu : 0.f;
-            const float dg[2] = {dcs[2 * lane] + down + before + all, dcs[2 * lane + 1] + s1 + after + before + z0 + all};
+            const float dg[2] = {s.dcs[2 * lane] + down + before + thr, s.dcs[2 * lane + 1] + s1 + after + before + z0 + thr};
             const float bias = a.bias ? a.bias[h] : 0.f, Ah = a.A[h];
             float sA = 0.f, sb = 0.f;
             for (int i = 0; i < 2; i++) {
                 const int row = 2 * lane + i;
                 if (row < valid) {
                     const size_t at = (tok + row) * a.Hv + h;
-                    const float raw = gdr_ld(static_cast<const bf16 *>(a.delta), at);
-                    sA = fmaf(dg[i], gdr_dt(raw, bias, a.softplus), sA);
-                    const float dd = dg[i] * Ah * (a.softplus ? gdr_sigmoid(raw + bias) : 1.f);
+                    const float pre = gdr_ld(static_cast<const bf16 *>(a.delta), at);
+                    sA = fmaf(dg[i], gdr_dt(pre, bias, a.softplus), sA);
+                    const float dd = dg[i] * Ah * (a.softplus ? gdr_sigmoid(pre + bias) : 1.f);
                     sb += dd;
-                    gdr_st(static_cast<bf16 *>(g.ddelta), at, dd);
-                    gdr_st(static_cast<bf16 *>(g.dbeta), at, db[row] * (a.sigmoid ? bb[row] * (1.f - bb[row]) : 1.f));
+                    gdr_st(static_cast<bf16 *>(ga.ddelta), at, dd);
+                    const float db = all(0, row) + all(2, row);
+                    gdr_st(static_cast<bf16 *>(ga.dbeta), at, db * (a.sigmoid ? bb[row] * (1.f - bb[row]) : 1.f));
                 }
             }
             sA = warp_sum(sA);
             sb = warp_sum(sb);
-            if (lane == 0) {   // parts: (2, B NC, Hv)
+            if (lane == 0) {   // (2, B NC, Hv)
                 const size_t at = ((size_t)b * lay.NC + n) * a.Hv + h;
-                parts[at] = sA;
-                parts[(size_t)a.Bsz * lay.NC * a.Hv + at] = sb;
+                partial[at] = sA;
+                partial[(size_t)a.Bsz * lay.NC * a.Hv + at] = sb;
             }
         }
     }
     // through the norms: d k = rk (dk^ - k^ (k^ . dk^))
-    const float inv = a.l2norm ? 1.f / a.scale : 0.f;
+    float kd[4] = {}, qd[4] = {};
+    dots(dK, m0, nK, Kt, kd);
+    dots(dQ, m0, nK, Qt, qd);
+    put_rows(4, kd);
+    put_rows(5, qd);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int row = ty + 16 * i;
-        float kd = 0.f, qd = 0.f;
+    for (int m = 0; m < 2; m++)
 #pragma unroll
-        for (int j = 0; j < RK; j++) {
-            kd = fmaf(Ks[row * pk + tx + 16 * j], dK[i][j], kd);
-            qd = fmaf(Qs[row * pk + tx + 16 * j], dQ[i][j], qd);
-        }
-        kd = a.l2norm ? row_add(kd) : 0.f;
-        qd = a.l2norm ? row_add(qd) * inv * inv : 0.f;   // Qs holds scale q^
-        if (row < valid)
+        for (int e = 0; e < 2; e++) {
+            const int row = m0 + 16 * m + gq + 8 * e;
+            if (row >= valid)
+                continue;
+            const float r = rk[row], f = rq[row], inv = a.scale != 0.f ? f / a.scale : 0.f;   // 1 / |k|, scale / |q|, 1 / |q|
+            const float ck = a.l2norm ? r * r * all(4, row) : 0.f, cq = a.l2norm ? inv * inv * all(5, row) : 0.f;
 #pragma unroll
-            for (int j = 0; j < RK; j++) {
-                const int c = tx + 16 * j;
-                const size_t at = ((tok + row) * a.Hk + hk) * K + c;
-                static_cast<bf16 *>(g.dk)[at] = __float2bfloat16_rn(rk[row] * fmaf(-Ks[row * pk + c], kd, dK[i][j]));
-                static_cast<bf16 *>(g.dq)[at] = __float2bfloat16_rn(rq[row] * fmaf(-Qs[row * pk + c], qd, dQ[i][j]));
+            for (int p = 0; p < NK; p++) {
+                const int j = nK + 8 * p + 2 * tq;
+                const size_t at = ((tok + row) * a.Hk + hk) * K + j;
+                *reinterpret_cast<__nv_bfloat162 *>(static_cast<bf16 *>(ga.dk) + at) = __floats2bfloat162_rn(
+                    r * fmaf(-Kt(row, j), ck, dK[m][p][2 * e]), r * fmaf(-Kt(row, j + 1), ck, dK[m][p][2 * e + 1]));
+                *reinterpret_cast<__nv_bfloat162 *>(static_cast<bf16 *>(ga.dq) + at) = __floats2bfloat162_rn(
+                    f * fmaf(-Qt(row, j), cq, dQ[m][p][2 * e]), f * fmaf(-Qt(row, j + 1), cq, dQ[m][p][2 * e + 1]));
             }
-    }
+        }
 }
 
 // ---- 5. dA and ddelta_bias: sums over batch and chunks, a warp per head
-__global__ void __launch_bounds__(32) head_sum_kernel(const float *parts, int64_t n, int Hv, float *dA, float *dbias)
+__global__ void __launch_bounds__(32) head_sum_kernel(const float *partial, int64_t n, int Hv, float *dA, float *dbias)
 {
     const int h = blockIdx.x;
     float s[2] = {0.f, 0.f};
     for (int64_t k = threadIdx.x; k < n; k += 32)
         for (int i = 0; i < 2; i++)
-            s[i] += parts[((size_t)i * n + k) * Hv + h];
+            s[i] += partial[((size_t)i * n + k) * Hv + h];
     const float x = warp_sum(s[0]), y = warp_sum(s[1]);
     if (threadIdx.x == 0) {
         dA[h] = x;
@@ -589,13 +892,34 @@ Layout layout(const GdrArgs &a)
 }
 
 template <class Kern, class... Args>
-cudaError_t go(Kern kernel, int64_t blocks, size_t floats, cudaStream_t st, Args... args)
+cudaError_t go(Kern kernel, int64_t blocks, size_t bytes, cudaStream_t st, Args... args)
 {
-    const size_t bytes = floats * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     if (e != cudaSuccess)
         return e;
     kernel<<<(unsigned)blocks, kThreads, bytes, st>>>(args...);
+    return cudaGetLastError();
+}
+
+template <int K, int V> cudaError_t launch(const GdrBwdArgs &g, cudaStream_t st)
+{
+    static_assert(sizeof(GradSmem<K, V>) <= 227 * 1024 && sizeof(PrepSmem<K, V>) <= 227 * 1024 &&
+                      sizeof(ReverseSmem<K>) <= 227 * 1024,
+                  "shared memory of one block");
+    const GdrArgs &a = g.f;
+    const Layout l = layout(a);
+    float *partial = static_cast<float *>(a.workspace) + (size_t)l.heads * l.NC * l.per();
+    const int64_t chains = l.heads * (V / kSlice);
+    cudaError_t e = go(prep_kernel<K, V>, l.heads * l.NC, sizeof(PrepSmem<K, V>), st, g, l);
+    if (e == cudaSuccess)
+        e = go(chain_kernel<K>, chains, sizeof(ChainSmem<K>), st, a, l);
+    if (e == cudaSuccess)
+        e = go(reverse_kernel<K>, chains, sizeof(ReverseSmem<K>), st, g, l);
+    if (e == cudaSuccess)
+        e = go(grad_kernel<K, V>, (int64_t)a.Bsz * a.Hk * l.NC, sizeof(GradSmem<K, V>), st, g, l, partial);
+    if (e != cudaSuccess)
+        return e;
+    head_sum_kernel<<<a.Hv, 32, 0, st>>>(partial, (int64_t)a.Bsz * l.NC, a.Hv, g.dA, g.dbias);
     return cudaGetLastError();
 }
 
@@ -609,32 +933,9 @@ size_t gdr_bwd_ws_bytes(const GdrArgs &a)
 
 cudaError_t launch_gdr_bwd(const GdrBwdArgs &g, cudaStream_t st)
 {
-    const GdrArgs &a = g.f;
-    const Layout l = layout(a);
-    float *parts = static_cast<float *>(a.workspace) + (size_t)l.heads * l.NC * l.per();
-    const size_t pk = a.K + 1, pv = a.V + 1, ps = kSlice + 1;
-    cudaError_t e = go(prep_kernel, l.heads * l.NC, 2 * kC * pk + kC * pv + 2 * kC * 65 + 4 * kC, st, a, l);
-    const int64_t chains = l.heads * (a.V / kSlice);
-    const size_t cf = 2 * kC * pk + kSlice * pk + kC * ps;
-    if (e == cudaSuccess)
-        e = a.K == 128 ? go(chain_kernel<128>, chains, cf, st, a, l) : go(chain_kernel<64>, chains, cf, st, a, l);
-    const size_t rf = 3 * kC * pk + kSlice * pk + 2 * kC * ps + kC * 65;
-    if (e == cudaSuccess)
-        e = a.K == 128 ? go(reverse_kernel<128>, chains, rf, st, g, l) : go(reverse_kernel<64>, chains, rf, st, g, l);
-    const int64_t blocks = (int64_t)a.Bsz * a.Hk * l.NC;
-    const size_t gf = 2 * kC * pk + 3 * kC * pv + kC * 65 + 8 * kC + 16;
-    if (e == cudaSuccess) {
-        if (a.K == 128)
-            e = a.V == 128 ? go(grad_kernel<128, 128>, blocks, gf, st, g, l, parts)
-                           : go(grad_kernel<128, 64>, blocks, gf, st, g, l, parts);
-        else
-            e = a.V == 128 ? go(grad_kernel<64, 128>, blocks, gf, st, g, l, parts)
-                           : go(grad_kernel<64, 64>, blocks, gf, st, g, l, parts);
-    }
-    if (e != cudaSuccess)
-        return e;
-    head_sum_kernel<<<a.Hv, 32, 0, st>>>(parts, (int64_t)a.Bsz * l.NC, a.Hv, g.dA, g.dbias);
-    return cudaGetLastError();
+    if (g.f.K == 128)
+        return g.f.V == 128 ? launch<128, 128>(g, st) : launch<128, 64>(g, st);
+    return g.f.V == 128 ? launch<64, 128>(g, st) : launch<64, 64>(g, st);
 }
 
 }  // namespace ssm
