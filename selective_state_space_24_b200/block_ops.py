@@ -68,30 +68,41 @@ SIGNATURES = {
 }
 
 
+def _raw_stream(torch, index):
+    """The handle of the device's current stream."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without building a Stream object
+    return torch.cuda.current_stream(index).cuda_stream if get is None else get(index)
+
+
 class _Call:
     """One call's device, stream and temporaries."""
 
     def __init__(self, x, name, stream):
         if not x.is_cuda:
             raise ValueError(f"{name}: tensors must be on a CUDA device")
-        self.torch = _torch()
+        self.torch = torch = _torch()
         self.name, self.device, self.dtype, self.code = name, x.device, x.dtype, _dtype_code(x)
-        self.f32, self.stream = self.torch.float32, stream
+        self.index, self.f32, self.stream = x.get_device(), torch.float32, stream
         self.made = []   # allocated here, to be kept for a stream that is not the current one
 
     def ptr(self, t, what, shape, dtype):
         """The address of t after its checks (None for None)."""
         if t is None:
             return None
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.get_device() == self.index and t.is_contiguous():
+            return t.data_ptr()
         if t.dtype != dtype:
             raise TypeError(f"{self.name}: {what} must be {dtype}, got {t.dtype}")
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{self.name}: {what} must have shape {shape}, got {tuple(t.shape)}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{self.name}: {what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
         if t.device != self.device:
             raise ValueError(f"{self.name}: {what} must be on {self.device}, got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{self.name}: {what} must be contiguous")
-        return t.data_ptr()
+        raise ValueError(f"{self.name}: {what} must be contiguous")
+
+    def like(self, t):
+        t = self.torch.empty_like(t)
+        self.made.append(t)
+        return t
 
     def new(self, shape, dtype):
         t = self.torch.empty(shape, dtype=dtype, device=self.device)
@@ -111,36 +122,42 @@ class _Call:
     def run(self, fn, *args):
         """fn(*args, stream) on the tensors' device; raises on an error."""
         cuda = self.torch.cuda
-        if self.device.index != cuda.current_device():
+        if self.index != cuda.current_device():
             with cuda.device(self.device):
                 return self._run(fn, args)
         return self._run(fn, args)
 
     def _run(self, fn, args):
-        here = self.torch.cuda.current_stream(self.device)
-        s = here if self.stream is None else self.stream
-        status = fn(*args, s.cuda_stream)
+        if self.stream is None:
+            status = fn(*args, _raw_stream(self.torch, self.index))
+        else:
+            status = fn(*args, self.stream.cuda_stream)
+            if self.stream != self.torch.cuda.current_stream(self.index):
+                for t in self.made:
+                    t.record_stream(self.stream)
         if status != 0:
             raise SSMError(status, self.name)
-        if s != here:
-            for t in self.made:
-                t.record_stream(s)
 
 
 def _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm, scale, step):
-    """dims, inputs and the shapes of the leading and of the state dimensions."""
+    """dims, inputs and the state's shape."""
+    qs, vs = q.shape, v.shape
     want = 3 if step else 4
-    if q.dim() != want or v.dim() != want:
+    if len(qs) != want or len(vs) != want:
         raise ValueError(f"{call.name}: q, k and v must have {want} dimensions")
-    lead, (Hk, K), (Hv, V) = tuple(q.shape[:-2]), q.shape[-2:], v.shape[-2:]
-    dims = gdr_dims(lead[0], 1 if step else lead[1], Hk, Hv, K, V, call.code)
-    f32, dt = call.f32, call.dtype
-    inp = gdr_inputs(call.ptr(q, "q", (*lead, Hk, K), dt), call.ptr(k, "k", (*lead, Hk, K), dt),
-                     call.ptr(v, "v", (*lead, Hv, V), dt), call.ptr(delta, "delta", (*lead, Hv), dt),
-                     call.ptr(delta_bias, "delta_bias", (Hv,), f32), call.ptr(A, "A", (Hv,), f32),
-                     call.ptr(beta, "beta", (*lead, Hv), dt), K ** -0.5 if scale is None else scale,
-                     int(bool(delta_softplus)), int(bool(beta_sigmoid)), int(bool(qk_l2norm)))
-    return dims, inp, lead, (lead[0], Hv, V, K)
+    if step:
+        (B, Hk, K), L, (Hv, V) = qs, 1, vs[1:]
+        vs_want, per = (B, Hv, V), (B, Hv)
+    else:
+        (B, L, Hk, K), (Hv, V) = qs, vs[2:]
+        vs_want, per = (B, L, Hv, V), (B, L, Hv)
+    ptr, f32, dt, head = call.ptr, call.f32, call.dtype, (Hv,)
+    dims = gdr_dims(B, L, Hk, Hv, K, V, call.code)
+    inp = gdr_inputs(ptr(q, "q", qs, dt), ptr(k, "k", qs, dt), ptr(v, "v", vs_want, dt), ptr(delta, "delta", per, dt),
+                     ptr(delta_bias, "delta_bias", head, f32), ptr(A, "A", head, f32), ptr(beta, "beta", per, dt),
+                     K ** -0.5 if scale is None else scale, 1 if delta_softplus else 0, 1 if beta_sigmoid else 0,
+                     1 if qk_l2norm else 0)
+    return dims, inp, (B, Hv, V, K)
 
 
 def gdr_chunk_fwd(q, k, v, delta, A, beta, *, delta_bias=None, delta_softplus=True, beta_sigmoid=True,
@@ -150,15 +167,15 @@ def gdr_chunk_fwd(q, k, v, delta, A, beta, *, delta_bias=None, delta_softplus=Tr
     (B, L, Hv, V).  initial_state and last_state (B, Hv, V, K) float32 may be
     the same tensor.  scale defaults to K ** -0.5."""
     call = _Call(q, "gdr_chunk_fwd", stream)
-    dims, inp, lead, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
+    dims, inp, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
                                scale, False)
     if out is None:
-        out = call.new(v.shape, v.dtype)
+        out = call.like(v)
     lib = capi()
     f32 = call.f32
     w, n = call.workspace(lib.gdr_chunk_workspace_size(_ref(dims)), ws)
     call.run(lib.gdr_chunk_fwd, _ref(dims), _ref(inp), call.ptr(initial_state, "initial_state", st, f32),
-             call.ptr(out, "out", tuple(v.shape), call.dtype), call.ptr(last_state, "last_state", st, f32), w, n)
+             call.ptr(out, "out", v.shape, call.dtype), call.ptr(last_state, "last_state", st, f32), w, n)
     return out
 
 
@@ -168,12 +185,12 @@ def gdr_step(q, k, v, delta, A, beta, state, *, delta_bias=None, delta_softplus=
     float32 or bfloat16; state (B, Hv, V, K) float32 updated in place.
     Returns out (B, Hv, V)."""
     call = _Call(q, "gdr_step", stream)
-    dims, inp, lead, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
+    dims, inp, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
                                scale, True)
     if out is None:
-        out = call.new(v.shape, v.dtype)
+        out = call.like(v)
     call.run(capi().gdr_step, _ref(dims), _ref(inp), call.ptr(state, "state", st, call.f32),
-             call.ptr(out, "out", tuple(v.shape), call.dtype))
+             call.ptr(out, "out", v.shape, call.dtype))
     return out
 
 
@@ -184,21 +201,20 @@ def gdr_chunk_bwd(q, k, v, delta, A, beta, dout, *, delta_bias=None, delta_softp
     the inputs' type, dA and (with delta_bias) ddelta_bias float32, and with
     initial_state its gradient dinitial_state."""
     call = _Call(q, "gdr_chunk_bwd", stream)
-    dims, inp, lead, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
+    dims, inp, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
                                scale, False)
     f32 = call.f32
-    g = {"dq": call.new(q.shape, q.dtype), "dk": call.new(k.shape, k.dtype), "dv": call.new(v.shape, v.dtype),
-         "ddelta": call.new(delta.shape, delta.dtype), "dbeta": call.new(beta.shape, beta.dtype),
-         "dA": call.new(A.shape, f32)}
+    g = {"dq": call.like(q), "dk": call.like(k), "dv": call.like(v), "ddelta": call.like(delta),
+         "dbeta": call.like(beta), "dA": call.like(A)}
     if delta_bias is not None:
-        g["ddelta_bias"] = call.new(delta_bias.shape, f32)
+        g["ddelta_bias"] = call.like(delta_bias)
     if initial_state is not None:
-        g["dinitial_state"] = call.new(st, f32)
+        g["dinitial_state"] = call.like(initial_state)
     out = gdr_grads(**{n: t.data_ptr() for n, t in g.items()})
     lib = capi()
     w, n = call.workspace(lib.gdr_chunk_bwd_workspace_size(_ref(dims)), ws)
     call.run(lib.gdr_chunk_bwd, _ref(dims), _ref(inp), call.ptr(initial_state, "initial_state", st, f32),
-             call.ptr(dout, "dout", tuple(v.shape), call.dtype), call.ptr(dlast_state, "dlast_state", st, f32),
+             call.ptr(dout, "dout", v.shape, call.dtype), call.ptr(dlast_state, "dlast_state", st, f32),
              _ref(out), w, n)
     return g
 
@@ -219,8 +235,8 @@ def gated_norm_fwd(x, weight, *, z=None, group=None, eps=1e-5, norm_before_gate=
     call = _Call(x, "gated_norm_fwd", stream)
     dims = _rows(call, x, weight, group, eps)
     if out is None:
-        out = call.new(x.shape, x.dtype)
-    shape = tuple(x.shape)
+        out = call.like(x)
+    shape = x.shape
     call.run(capi().gated_norm_fwd, _ref(dims), call.ptr(x, "x", shape, call.dtype), call.ptr(z, "z", shape, call.dtype),
              call.ptr(weight, "weight", shape[-1:], call.f32), int(bool(norm_before_gate)),
              call.ptr(out, "out", shape, call.dtype))
@@ -232,10 +248,10 @@ def gated_norm_bwd(x, weight, dout, *, z=None, group=None, eps=1e-5, norm_before
     dweight float32."""
     call = _Call(x, "gated_norm_bwd", stream)
     dims = _rows(call, x, weight, group, eps)
-    shape, dt = tuple(x.shape), call.dtype
-    g = {"dx": call.new(shape, dt), "dweight": call.new(shape[-1:], call.f32)}
+    shape, dt = x.shape, call.dtype
+    g = {"dx": call.like(x), "dweight": call.like(weight)}
     if z is not None:
-        g["dz"] = call.new(shape, dt)
+        g["dz"] = call.like(z)
     lib = capi()
     w, n = call.workspace(lib.gated_norm_bwd_workspace_size(_ref(dims)), ws)
     call.run(lib.gated_norm_bwd, _ref(dims), call.ptr(x, "x", shape, dt), call.ptr(z, "z", shape, dt),
@@ -247,7 +263,7 @@ def gated_norm_bwd(x, weight, dout, *, z=None, group=None, eps=1e-5, norm_before
 
 def _residual(call, x, weight, bias, scale, post_weight, alpha, layer_norm, residual_f32, eps):
     dims = _rows(call, x, weight, None, eps)
-    one, f32 = tuple(x.shape[-1:]), call.f32
+    one, f32 = x.shape[-1:], call.f32
     samples = 1
     if scale is not None:
         if scale.dim() == 1:
@@ -271,11 +287,11 @@ def residual_norm_fwd(x, weight, *, residual=None, bias=None, scale=None, post_w
     into `samples` equal runs.  Returns (out, residual_out)."""
     call = _Call(x, "residual_norm_fwd", stream)
     dims, p, rt = _residual(call, x, weight, bias, scale, post_weight, alpha, layer_norm, residual_f32, eps)
-    shape, dt = tuple(x.shape), call.dtype
+    shape, dt = x.shape, call.dtype
     if out is None:
-        out = call.new(shape, dt)
+        out = call.like(x)
     if residual_out is None:
-        residual_out = call.new(shape, rt)
+        residual_out = call.like(x if rt == dt else residual) if rt == dt or residual is not None else call.new(shape, rt)
     call.run(capi().residual_norm_fwd, _ref(dims), _ref(p), call.ptr(x, "x", shape, dt),
              call.ptr(residual, "residual", shape, rt), call.ptr(residual_out, "residual_out", shape, rt),
              call.ptr(out, "out", shape, dt))
@@ -293,13 +309,13 @@ def residual_norm_bwd(x, residual_out, weight, dout, *, dresidual_out=None, need
         raise TypeError(f"{call.name}: residual_out must be float32 or {call.dtype}, got {residual_out.dtype}")
     dims, p, rt = _residual(call, x, weight, bias, scale, post_weight, alpha, layer_norm,
                             residual_out.dtype == call.f32, eps)
-    shape, dt, f32 = tuple(x.shape), call.dtype, call.f32
-    g = {"dx": call.new(shape, dt), "dweight": call.new(weight.shape, f32)}
+    shape, dt = x.shape, call.dtype
+    g = {"dx": call.like(x), "dweight": call.like(weight)}
     if need_dresidual:
-        g["dresidual"] = call.new(shape, rt)
+        g["dresidual"] = call.like(residual_out)
     for name, t in (("dbias", bias), ("dscale", scale), ("dpost_weight", post_weight)):
         if t is not None:
-            g[name] = call.new(t.shape, f32)
+            g[name] = call.like(t)
     c = residual_norm_grads(**{n: t.data_ptr() for n, t in g.items()})
     lib = capi()
     w, n = call.workspace(lib.residual_norm_bwd_workspace_size(_ref(dims), _ref(p)), ws)

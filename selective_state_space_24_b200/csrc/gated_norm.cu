@@ -18,20 +18,17 @@
 namespace ssm {
 namespace {
 
-NormPlan gated_plan(int64_t rows, int dim, int group)
+// Blocks for the rows of one group: as many as rows, at most `most` in all.
+int64_t parts_for(int64_t rows, int64_t groups, const NormPlan &p, int64_t most)
 {
-    const int G = dim / group;
-    NormPlan p = norm_threads(group);
-    const int64_t need = (rows + p.rows_at_once - 1) / p.rows_at_once;
-    const int64_t most = ((int64_t)148 * (2048 / p.threads) + G - 1) / G;
-    p.parts = (int)(need < most ? need : most);
-    return p;
+    const int64_t need = (rows + p.rows_at_once - 1) / p.rows_at_once, share = most / groups;
+    return share < 1 ? 1 : need < share ? need : share;
 }
 
-template <typename T, bool BWD>
+template <typename T, int ELEMS, bool BWD>
 __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int tpr, int rpb, int parts)
 {
-    constexpr int E = Vec<T>::N, NV = kNormElems / E;
+    constexpr int E = Vec<T>::N, NV = ELEMS / E;
     __shared__ RedSmem red;
     extern __shared__ float cols[];   // (group), backward only
     const int lane_r = threadIdx.x % tpr, sub = threadIdx.x / tpr;
@@ -54,25 +51,30 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
         if (in[v])
             load_f32<E>(a.weight + col + (lane_r + v * tpr) * E, w[v]);
     }
+    Raw<T, NV, E> xr, zr, dr;   // of the next row
+    auto fetch = [&](int64_t r0) {
+        const bool live = r0 + sub < a.rows;
+        const int64_t base = live ? (r0 + sub) * a.dim + col : 0;
+        xr.load(x + base, lane_r, tpr, in, live);
+        if (z)
+            zr.load(z + base, lane_r, tpr, in, live);
+        if (BWD)
+            dr.load(dout + base, lane_r, tpr, in, live);
+    };
+    const int64_t stride = (int64_t)parts * rpb;
+    fetch((int64_t)part * rpb);
     // every thread of the block takes the same number of turns (barriers)
-    for (int64_t r0 = (int64_t)part * rpb; r0 < a.rows; r0 += (int64_t)parts * rpb) {
+    for (int64_t r0 = (int64_t)part * rpb; r0 < a.rows; r0 += stride) {
         const bool live = r0 + sub < a.rows;
         const int64_t base = (r0 + sub) * a.dim + col;
         float xv[NV][E], zv[NV][E], dv[NV][E];
-#pragma unroll
-        for (int v = 0; v < NV; v++) {
-            const int64_t at = base + (lane_r + v * tpr) * E;
-#pragma unroll
-            for (int e = 0; e < E; e++)
-                xv[v][e] = zv[v][e] = dv[v][e] = 0.f;
-            if (live && in[v]) {
-                Vec<T>::load(x + at, xv[v]);
-                if (z)
-                    Vec<T>::load(z + at, zv[v]);
-                if (BWD)
-                    Vec<T>::load(dout + at, dv[v]);
-            }
-        }
+        xr.get(xv);
+        if (z)
+            zr.get(zv);
+        if (BWD)
+            dr.get(dv);
+        if (r0 + stride < a.rows)
+            fetch(r0 + stride);
         float sg[NV][E];   // sigmoid(z)
         float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -117,9 +119,9 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
                 }
             }
             if (live && in[v]) {
-                Vec<T>::store(static_cast<T *>(BWD ? a.dx : a.out) + at, o);
+                store_row<T, E>(static_cast<T *>(BWD ? a.dx : a.out) + at, o);
                 if (BWD && z)
-                    Vec<T>::store(static_cast<T *>(a.dz) + at, oz);
+                    store_row<T, E>(static_cast<T *>(a.dz) + at, oz);
             }
         }
     }
@@ -144,67 +146,83 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
     }
 }
 
-template <typename T, bool BWD> cudaError_t launch_typed(const GatedArgs &a, cudaStream_t st)
+// parts: how many blocks shared the rows of a group (for the column sums)
+template <typename T, bool BWD> cudaError_t launch_typed(const GatedArgs &a, cudaStream_t st, int *parts)
 {
-    const NormPlan p = gated_plan(a.rows, a.dim, a.group);
-    const unsigned blocks = (unsigned)p.parts * (unsigned)(a.dim / a.group);
-    gated_norm_kernel<T, BWD><<<blocks, p.threads, BWD ? a.group * sizeof(float) : 0, st>>>(a, p.tpr, p.rows_at_once, p.parts);
+    const NormPlan p = norm_threads(a.group);
+    const int G = a.dim / a.group;
+    const size_t smem = BWD ? a.group * sizeof(float) : 0;
+    auto go = [&](auto kernel) {
+        *parts = (int)parts_for(a.rows, G, p, resident_blocks(kernel, p.threads, smem));
+        kernel<<<(unsigned)(*parts * G), p.threads, smem, st>>>(a, p.tpr, p.rows_at_once, *parts);
+    };
+    p.elems == 8 ? go(gated_norm_kernel<T, 8, BWD>) : go(gated_norm_kernel<T, 16, BWD>);
     return cudaGetLastError();
 }
 
-// 32 columns x 8 strands of partial rows; the strands are joined in order
-__global__ void __launch_bounds__(256) part_sum_kernel(const float *parts, int nparts, int dim, float *out)
+struct Sums {
+    PartSum s[kMaxSums];
+};
+// Block: 32 columns x 32 strands of the partial rows of one sum and set; the
+// strands are joined in order.
+__global__ void __launch_bounds__(1024) part_sum_kernel(const Sums sums, int dim)
 {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
+    const PartSum &j = sums.s[blockIdx.z];
     const int c = blockIdx.x * 32 + threadIdx.x;
-    const float *p = parts + (size_t)blockIdx.y * nparts * dim;
-    float v = 0.f;
-    if (c < dim)
-        for (int k = threadIdx.y; k < nparts; k += 8)
-            v += p[(size_t)k * dim + c];
-    s[threadIdx.y][threadIdx.x] = v;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < dim) {
-        float t = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-            t += s[k][threadIdx.x];
-        out[(size_t)blockIdx.y * dim + c] = t;
+    for (int64_t set = blockIdx.y; set < j.sets; set += gridDim.y) {
+        const float *p = j.parts + (size_t)set * j.nparts * dim;
+        float v = 0.f;
+        if (c < dim)
+            for (int k = threadIdx.y; k < j.nparts; k += 32)
+                v += p[(size_t)k * dim + c];
+        s[threadIdx.y][threadIdx.x] = v;
+        __syncthreads();
+        // warp y sums column y of the block over the strands
+        const float t = warp_add(s[threadIdx.x][threadIdx.y]);
+        const int col = blockIdx.x * 32 + threadIdx.y;
+        if (threadIdx.x == 0 && col < dim)
+            j.out[(size_t)set * dim + col] = t;
+        __syncthreads();
     }
 }
 
 }  // namespace
 
-cudaError_t launch_part_sum(const float *parts, int64_t sets, int nparts, int dim, float *out, cudaStream_t st)
+cudaError_t launch_part_sums(const PartSum *sums, int n, int dim, cudaStream_t st)
 {
-    for (int64_t s = 0; s < sets; s += 65535) {
-        const unsigned n = (unsigned)(sets - s < 65535 ? sets - s : 65535);
-        part_sum_kernel<<<dim3((dim + 31) / 32, n), dim3(32, 8), 0, st>>>(parts + (size_t)s * nparts * dim, nparts, dim,
-                                                                         out + (size_t)s * dim);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess)
-            return e;
+    Sums j;
+    int64_t most = 1;
+    for (int k = 0; k < n; k++) {
+        j.s[k] = sums[k];
+        most = sums[k].sets > most ? sums[k].sets : most;
     }
-    return cudaSuccess;
+    const dim3 grid((dim + 31) / 32, (unsigned)(most < 65535 ? most : 65535), n);
+    part_sum_kernel<<<grid, dim3(32, 32), 0, st>>>(j, dim);
+    return cudaGetLastError();
 }
 
 size_t gated_bwd_workspace(int64_t rows, int dim, int group)
 {
-    return (size_t)gated_plan(rows, dim, group).parts * dim * sizeof(float);
+    const NormPlan p = norm_threads(group);
+    return (size_t)parts_for(rows, dim / group, p, (int64_t)kSMs * (2048 / p.threads)) * dim * sizeof(float);
 }
 
 cudaError_t launch_gated_fwd(const GatedArgs &a, cudaStream_t st)
 {
-    return a.dtype == 0 ? launch_typed<float, false>(a, st) : launch_typed<__nv_bfloat16, false>(a, st);
+    int parts;
+    return a.dtype == 0 ? launch_typed<float, false>(a, st, &parts) : launch_typed<__nv_bfloat16, false>(a, st, &parts);
 }
 
 cudaError_t launch_gated_bwd(const GatedArgs &a, cudaStream_t st)
 {
+    int parts = 0;
     const cudaError_t e =
-        a.dtype == 0 ? launch_typed<float, true>(a, st) : launch_typed<__nv_bfloat16, true>(a, st);
+        a.dtype == 0 ? launch_typed<float, true>(a, st, &parts) : launch_typed<__nv_bfloat16, true>(a, st, &parts);
     if (e != cudaSuccess)
         return e;
-    return launch_part_sum(a.parts, 1, gated_plan(a.rows, a.dim, a.group).parts, a.dim, a.dweight, st);
+    const PartSum sum{a.parts, a.dweight, 1, parts};
+    return launch_part_sums(&sum, 1, a.dim, st);
 }
 
 }  // namespace ssm

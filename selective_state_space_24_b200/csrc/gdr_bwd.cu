@@ -82,8 +82,7 @@ __device__ __forceinline__ uint32_t tf32(float x)
 }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
@@ -103,14 +102,28 @@ template <Part P, int N> __device__ __forceinline__ void parts(const float (&x)[
 
 // A warp's tile: acc += a(m0 + .., k) b(k, n0 + ..), MT x 16 rows, NT x 8
 // columns.  Element e of acc[m][n] is row m0 + 16 m + lane / 4 + 8 (e / 2),
-// column n0 + 8 n + 2 (lane mod 4) + e mod 2.
+// column n0 + 8 n + 2 (lane mod 4) + e mod 2.  The products of one part go
+// over the whole tile before those of the next, so that an accumulator is not
+// waited for; tiles of few accumulators keep one set for each part.
 template <Part PA, Part PB, int MT, int NT, class FA, class FB>
 __device__ __forceinline__ void mm(float (&acc)[MT][NT][4], int m0, int n0, int kdim, FA a, FB b)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr bool kApart = MT * NT <= 4;
+    float other[2][kApart ? MT : 1][kApart ? NT : 1][4];
+    if (kApart)
+#pragma unroll
+        for (int s = 0; s < 2; s++)
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        other[s][m * kApart][n * kApart][e] = 0.f;
 #pragma unroll 2
     for (int k = 0; k < kdim; k += 8) {
-        uint32_t ah[MT][4], al[MT][4];
+        uint32_t ah[MT][4], al[MT][4], bh[NT][2], bl[NT][2];
 #pragma unroll
         for (int m = 0; m < MT; m++) {
             const int r = m0 + 16 * m + g;
@@ -121,18 +134,34 @@ __device__ __forceinline__ void mm(float (&acc)[MT][NT][4], int m0, int n0, int 
         for (int n = 0; n < NT; n++) {
             const int c = n0 + 8 * n + g;
             const float y[2] = {b(k + t, c), b(k + t + 4, c)};
-            uint32_t bh[2], bl[2];
-            parts<PB>(y, bh, bl);
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-                if (PB == kTwo)
-                    mma(acc[m][n], ah[m], bl);
-                if (PA == kTwo)
-                    mma(acc[m][n], al[m], bh);
-                mma(acc[m][n], ah[m], bh);
-            }
+            parts<PB>(y, bh[n], bl[n]);
         }
+        if (PB == kTwo)
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+                    mma(kApart ? other[0][m * kApart][n * kApart] : acc[m][n], ah[m], bl[n]);
+        if (PA == kTwo)
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+                for (int n = 0; n < NT; n++)
+                    mma(kApart ? other[1][m * kApart][n * kApart] : acc[m][n], al[m], bh[n]);
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+                mma(acc[m][n], ah[m], bh[n]);
     }
+    if (kApart)
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    acc[m][n][e] += other[0][m * kApart][n * kApart][e] + other[1][m * kApart][n * kApart][e];
 }
 template <int MT, int NT> __device__ __forceinline__ void zero(float (&acc)[MT][NT][4])
 {

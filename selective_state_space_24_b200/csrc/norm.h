@@ -8,15 +8,14 @@
 namespace ssm {
 
 // How threads cover rows (of one group of columns): tpr threads per row, a
-// power of two, each holding 16 elements; up to 32 threads per row a block
-// works on threads / tpr rows at a time, beyond that on one.  Block b owns
-// the columns of group b % G and walks rows with a stride, so a thread's
+// power of two, each holding `elems` elements; a block works on threads / tpr
+// rows at a time.  Block b owns the columns of group b % G and walks rows with a stride, so a thread's
 // columns never change: its weights stay in registers and column sums gather
-// there.  `parts` blocks share the rows of one group (or sample).
+// there.  Several blocks share the rows of one group (or sample), each
+// with a partial sum of its own.
 struct NormPlan {
-    int tpr, threads;
+    int elems, tpr, threads;
     int rows_at_once;   // rows a block works on at a time
-    int parts;
 };
 
 struct GatedArgs {
@@ -48,7 +47,15 @@ size_t residual_bwd_workspace(int64_t rows, int64_t samples, int dim, bool has_b
 cudaError_t launch_residual_fwd(const ResidualArgs &a, cudaStream_t st);
 cudaError_t launch_residual_bwd(const ResidualArgs &a, cudaStream_t st);
 
-// out[s][c] = sum over p of parts[s][p][c], in a fixed order
-cudaError_t launch_part_sum(const float *parts, int64_t sets, int nparts, int dim, float *out, cudaStream_t st);
+// Sums of partial rows, several at once: out[s][c] = sum over p < nparts of
+// parts[s][p][c] for s < sets, in a fixed order.
+struct PartSum {
+    const float *parts;
+    float *out;
+    int64_t sets;
+    int nparts;
+};
+constexpr int kMaxSums = 4;
+cudaError_t launch_part_sums(const PartSum *sums, int n, int dim, cudaStream_t st);
 
 }  // namespace ssm

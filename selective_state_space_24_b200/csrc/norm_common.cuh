@@ -1,5 +1,4 @@
-// norm_common.cuh -- what the norm kernels share: vectors of 16 bytes held
-// as float32, sums over the threads of one row (or group), and the sum of
+// norm_common.cuh -- what the norm kernels share: a thread's part of a row, sums over the threads of one row (or group), and the sum of
 // per-CTA partial column sums.
 #pragma once
 
@@ -15,21 +14,19 @@ namespace ssm {
 template <typename T> struct Vec;   // 16 bytes of T
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, float (&f)[4])
+    static __device__ __forceinline__ void unpack(const uint4 &v, float *f)
     {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+        f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
     }
-    static __device__ __forceinline__ void store(float *p, const float (&f)[4])
+    static __device__ __forceinline__ uint4 pack(const float *f)
     {
-        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float (&f)[8])
+    static __device__ __forceinline__ void unpack(const uint4 &v, float *f)
     {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; k++) {
@@ -37,7 +34,7 @@ template <> struct Vec<__nv_bfloat16> {
             f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[8])
+    static __device__ __forceinline__ uint4 pack(const float *f)
     {
         uint32_t u[4];
 #pragma unroll
@@ -45,24 +42,66 @@ template <> struct Vec<__nv_bfloat16> {
             const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
             u[k] = *reinterpret_cast<const uint32_t *>(&h);
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        return make_uint4(u[0], u[1], u[2], u[3]);
     }
 };
 
-constexpr int kNormElems = 16;      // elements of a row that one thread holds
-constexpr int kNormMaxLen = 8192;   // elements normed together: 512 threads of 16
+// This thread's elements of one row of R as they lie in memory: NV vectors of
+// N elements (N as the call's type has in 16 bytes), held until they are used,
+// so that the next row's are on their way during the work on this one.
+template <typename R, int NV, int N> struct Raw {
+    static constexpr int W = N / Vec<R>::N;   // 16-byte words per vector
+    uint4 w[NV][W];
+    // vectors lane_r, lane_r + tpr, .. of the row at p; zeros outside it (on[v] false)
+    __device__ __forceinline__ void load(const R *p, int lane_r, int tpr, const bool (&on)[NV], bool live)
+    {
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int k = 0; k < W; k++)
+                w[v][k] = live && on[v]
+                              ? reinterpret_cast<const uint4 *>(p + (lane_r + v * tpr) * N)[k]
+                              : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&f)[NV][N]) const
+    {
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int k = 0; k < W; k++)
+                Vec<R>::unpack(w[v][k], &f[v][k * Vec<R>::N]);
+    }
+};
+template <typename R, int N> __device__ __forceinline__ void store_row(R *p, const float (&f)[N])
+{
+#pragma unroll
+    for (int k = 0; k < N / Vec<R>::N; k++)
+        reinterpret_cast<uint4 *>(p)[k] = Vec<R>::pack(&f[k * Vec<R>::N]);
+}
+
+constexpr int kSMs = 148;
 
 // Threads for rows of `len` elements normed together.
 inline NormPlan norm_threads(int len)
 {
     NormPlan p;
+    p.elems = len <= 4096 ? 8 : 16;   // up to 512 threads a row
     p.tpr = 1;
-    while (p.tpr * kNormElems < len)
+    while (p.tpr * p.elems < len)
         p.tpr *= 2;
     p.threads = p.tpr > 128 ? p.tpr : 128;
     p.rows_at_once = p.threads / p.tpr;
-    p.parts = 1;
     return p;
+}
+
+// Blocks of a kernel that the GPU holds at once: blocks that walk their rows
+// with a stride are launched that often, so that all of them end together.
+template <class Kern> int64_t resident_blocks(Kern kernel, int threads, size_t smem)
+{
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1)
+        n = 1;
+    return (int64_t)kSMs * n;
 }
 
 // N consecutive float32 (weights next to a vector of N elements)
@@ -74,38 +113,6 @@ template <int N> __device__ __forceinline__ void load_f32(const float *p, float 
         f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
     }
 }
-template <int N> __device__ __forceinline__ void store_f32(float *p, const float (&f)[N])
-{
-#pragma unroll
-    for (int k = 0; k < N; k += 4)
-        *reinterpret_cast<float4 *>(p + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
-}
-
-// N consecutive elements of the residual stream (float32 or bf16) next to a
-// vector of N elements of the call's type
-template <typename R, int N> __device__ __forceinline__ void load_row(const R *p, float (&f)[N])
-{
-#pragma unroll
-    for (int k = 0; k < N; k += Vec<R>::N) {
-        float t[Vec<R>::N];
-        Vec<R>::load(p + k, t);
-#pragma unroll
-        for (int i = 0; i < Vec<R>::N; i++)
-            f[k + i] = t[i];
-    }
-}
-template <typename R, int N> __device__ __forceinline__ void store_row(R *p, const float (&f)[N])
-{
-#pragma unroll
-    for (int k = 0; k < N; k += Vec<R>::N) {
-        float t[Vec<R>::N];
-#pragma unroll
-        for (int i = 0; i < Vec<R>::N; i++)
-            t[i] = f[k + i];
-        Vec<R>::store(p + k, t);
-    }
-}
-
 constexpr int kRedMax = 2;   // values summed at once
 // shared memory of row_sum: two buffers in turn, so that one barrier per sum
 // is enough (a buffer is written again only after the next sum's barrier)
@@ -145,7 +152,15 @@ template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], int tpr,
     }
 }
 
-// z sigmoid(z), and with it the sigmoid
+// the sum over a warp's lanes
+__device__ __forceinline__ float warp_add(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 __device__ __forceinline__ float sigmoid_f(float z) { return rcp_mufu(1.f + ex2_mufu(-z * kLog2e)); }
 
 }  // namespace ssm

@@ -21,13 +21,11 @@
 namespace ssm {
 namespace {
 
-NormPlan residual_plan(int64_t rows, int64_t sets, int dim)
+// Blocks for the rows of one set: as many as rows, at most `most` in all.
+int64_t parts_for(int64_t rows, int64_t sets, const NormPlan &p, int64_t most)
 {
-    NormPlan p = norm_threads(dim);
-    const int64_t need = (rows / sets + p.rows_at_once - 1) / p.rows_at_once;
-    const int64_t most = ((int64_t)148 * (2048 / p.threads) + sets - 1) / sets;
-    p.parts = (int)(need < most ? need : most);
-    return p;
+    const int64_t need = (rows / sets + p.rows_at_once - 1) / p.rows_at_once, share = most / sets;
+    return share < 1 ? 1 : need < share ? need : share;
 }
 
 // The sets of rows that never share a block: the samples where a scale's
@@ -87,10 +85,10 @@ template <> __device__ __forceinline__ float rounded<__nv_bfloat16>(float v)
     return __bfloat162float(__float2bfloat16_rn(v));
 }
 
-template <typename T, typename R, bool LAYER>
+template <typename T, typename R, int ELEMS, bool LAYER>
 __global__ void __launch_bounds__(512) residual_fwd_kernel(const ResidualArgs a, int tpr, int rpb)
 {
-    constexpr int E = Vec<T>::N, NV = kNormElems / E;
+    constexpr int E = Vec<T>::N, NV = ELEMS / E;
     __shared__ RedSmem red;
     const int lane_r = threadIdx.x % tpr, sub = threadIdx.x / tpr;
     const int nv = a.dim / E;
@@ -103,22 +101,26 @@ __global__ void __launch_bounds__(512) residual_fwd_kernel(const ResidualArgs a,
 #pragma unroll
     for (int v = 0; v < NV; v++)
         in[v] = lane_r + v * tpr < nv;
-    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += (int64_t)gridDim.x * rpb) {
+    Raw<T, NV, E> xr;   // of the next row
+    Raw<R, NV, E> rr;
+    auto fetch = [&](int64_t r0) {
+        const bool live = r0 + sub < a.rows;
+        const int64_t base = live ? (r0 + sub) * a.dim : 0;
+        xr.load(x + base, lane_r, tpr, in, live);
+        if (res)
+            rr.load(res + base, lane_r, tpr, in, live);
+    };
+    const int64_t stride = (int64_t)gridDim.x * rpb;
+    fetch((int64_t)blockIdx.x * rpb);
+    for (int64_t r0 = (int64_t)blockIdx.x * rpb; r0 < a.rows; r0 += stride) {
         const int64_t row = r0 + sub;
         const bool live = row < a.rows;
         float t[NV][E], rv[NV][E];
-#pragma unroll
-        for (int v = 0; v < NV; v++) {
-            const int64_t at = row * a.dim + (lane_r + v * tpr) * E;
-#pragma unroll
-            for (int e = 0; e < E; e++)
-                t[v][e] = rv[v][e] = 0.f;
-            if (live && in[v]) {
-                Vec<T>::load(x + at, t[v]);
-                if (res)
-                    load_row<R, E>(res + at, rv[v]);
-            }
-        }
+        xr.get(t);
+        if (res)
+            rr.get(rv);
+        if (r0 + stride < a.rows)
+            fetch(r0 + stride);
         if (a.post) {
             float s[1] = {0.f};
 #pragma unroll
@@ -168,16 +170,16 @@ __global__ void __launch_bounds__(512) residual_fwd_kernel(const ResidualArgs a,
 #pragma unroll
                 for (int e = 0; e < E; e++)
                     o[e] = fmaf(rv[v][e] * k, w[e], b[e]);
-                Vec<T>::store(static_cast<T *>(a.out) + row * a.dim + c, o);
+                store_row<T, E>(static_cast<T *>(a.out) + row * a.dim + c, o);
             }
     }
 }
 
 // A variant for each set of column sums (registers for the others are not kept).
-template <typename T, typename R, bool LAYER, bool BIAS, bool SCALE, bool POST>
+template <typename T, typename R, int ELEMS, bool LAYER, bool BIAS, bool SCALE, bool POST>
 __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a, int tpr, int rpb, int parts)
 {
-    constexpr int E = Vec<T>::N, NV = kNormElems / E;
+    constexpr int E = Vec<T>::N, NV = ELEMS / E;
     __shared__ RedSmem red;
     extern __shared__ float cols[];   // (dim)
     const int lane_r = threadIdx.x % tpr, sub = threadIdx.x / tpr;
@@ -204,21 +206,38 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
                 dpo[v][e] = 0.f;
         }
     }
-    for (int64_t r0 = set * per + (int64_t)part * rpb; r0 < row_end; r0 += (int64_t)parts * rpb) {
+    Raw<R, NV, E> yr, sr;   // of the next row
+    Raw<T, NV, E> gr, xr;
+    auto fetch = [&](int64_t r0) {
+        const bool live = r0 + sub < row_end;
+        const int64_t base = live ? (r0 + sub) * a.dim : 0;
+        yr.load(static_cast<const R *>(a.res_out) + base, lane_r, tpr, in, live);
+        gr.load(static_cast<const T *>(a.dout) + base, lane_r, tpr, in, live);
+        if (a.dres_out)
+            sr.load(static_cast<const R *>(a.dres_out) + base, lane_r, tpr, in, live);
+        if (SCALE || POST)
+            xr.load(static_cast<const T *>(a.x) + base, lane_r, tpr, in, live);
+    };
+    const int64_t stride = (int64_t)parts * rpb;
+    fetch(set * per + (int64_t)part * rpb);
+    for (int64_t r0 = set * per + (int64_t)part * rpb; r0 < row_end; r0 += stride) {
         const int64_t row = r0 + sub;
         const bool live = row < row_end;
         float y[NV][E], g[NV][E];   // the stream (then its norm), dout (then dr)
+        float d[NV][E], t[NV][E];   // the gradient of the stream's later uses, x
+        yr.get(y);
+        gr.get(g);
 #pragma unroll
-        for (int v = 0; v < NV; v++) {
-            const int64_t at = row * a.dim + (lane_r + v * tpr) * E;
+        for (int v = 0; v < NV; v++)
 #pragma unroll
             for (int e = 0; e < E; e++)
-                y[v][e] = g[v][e] = 0.f;
-            if (live && in[v]) {
-                load_row<R, E>(static_cast<const R *>(a.res_out) + at, y[v]);
-                Vec<T>::load(static_cast<const T *>(a.dout) + at, g[v]);
-            }
-        }
+                d[v][e] = 0.f;
+        if (a.dres_out)
+            sr.get(d);
+        if (SCALE || POST)
+            xr.get(t);
+        if (r0 + stride < row_end)
+            fetch(r0 + stride);
         const float k = norm_stats<LAYER>(y, in, inv, a.eps, tpr, red, turn);
         float s[2] = {0.f, 0.f};   // sums of g y and g
 #pragma unroll
@@ -243,30 +262,16 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
         for (int v = 0; v < NV; v++)
             if (live && in[v]) {
                 const int64_t at = row * a.dim + (lane_r + v * tpr) * E;
-                float d[E], o[E];
-#pragma unroll
-                for (int e = 0; e < E; e++)
-                    d[e] = 0.f;
-                if (a.dres_out)
-                    load_row<R, E>(static_cast<const R *>(a.dres_out) + at, d);
+                float o[E];
 #pragma unroll
                 for (int e = 0; e < E; e++) {
-                    g[v][e] = fmaf(k, fmaf(-y[v][e], mgy, g[v][e] - mg), d[e]);
+                    g[v][e] = fmaf(k, fmaf(-y[v][e], mgy, g[v][e] - mg), d[v][e]);
                     o[e] = a.alpha * g[v][e];
                 }
                 if (a.dres)
                     store_row<R, E>(static_cast<R *>(a.dres) + at, o);
             }
         if (SCALE || POST) {
-            float t[NV][E];   // x, normed with POST
-#pragma unroll
-            for (int v = 0; v < NV; v++) {
-#pragma unroll
-                for (int e = 0; e < E; e++)
-                    t[v][e] = 0.f;
-                if (live && in[v])
-                    Vec<T>::load(static_cast<const T *>(a.x) + row * a.dim + (lane_r + v * tpr) * E, t[v]);
-            }
             float p = 1.f;
             if (POST) {
                 float q[1] = {0.f};
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
 #pragma unroll
         for (int v = 0; v < NV; v++)
             if (live && in[v])
-                Vec<T>::store(static_cast<T *>(a.dx) + row * a.dim + (lane_r + v * tpr) * E, g[v]);
+                store_row<T, E>(static_cast<T *>(a.dx) + row * a.dim + (lane_r + v * tpr) * E, g[v]);
     }
     // partial column sums: kind after kind, (sets, parts, dim) each
     float *out = a.parts + (size_t)blockIdx.x * a.dim;
@@ -354,36 +359,45 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
 
 template <typename T, typename R> cudaError_t fwd_typed(const ResidualArgs &a, cudaStream_t st)
 {
-    const NormPlan p = residual_plan(a.rows, 1, a.dim);
-    if (a.layer)
-        residual_fwd_kernel<T, R, true><<<p.parts, p.threads, 0, st>>>(a, p.tpr, p.rows_at_once);
+    const NormPlan p = norm_threads(a.dim);
+    auto go = [&](auto kernel) {
+        const int64_t n = parts_for(a.rows, 1, p, resident_blocks(kernel, p.threads, 0));
+        kernel<<<(unsigned)n, p.threads, 0, st>>>(a, p.tpr, p.rows_at_once);
+    };
+    if (p.elems == 8)
+        a.layer ? go(residual_fwd_kernel<T, R, 8, true>) : go(residual_fwd_kernel<T, R, 8, false>);
     else
-        residual_fwd_kernel<T, R, false><<<p.parts, p.threads, 0, st>>>(a, p.tpr, p.rows_at_once);
+        a.layer ? go(residual_fwd_kernel<T, R, 16, true>) : go(residual_fwd_kernel<T, R, 16, false>);
     return cudaGetLastError();
 }
 
 template <typename T, typename R> cudaError_t bwd_typed(const ResidualArgs &a, cudaStream_t st)
 {
     const int64_t sets = row_sets(a.samples, a.scale != nullptr);
-    const NormPlan p = residual_plan(a.rows, sets, a.dim);
-    const unsigned blocks = (unsigned)(sets * p.parts);
-    auto go = [&](auto layer, auto bias, auto scale, auto post) {
-        residual_bwd_kernel<T, R, layer.value, bias.value, scale.value, post.value>
-            <<<blocks, p.threads, a.dim * sizeof(float), st>>>(a, p.tpr, p.rows_at_once, p.parts);
+    const NormPlan p = norm_threads(a.dim);
+    const size_t smem = a.dim * sizeof(float);
+    unsigned blocks = 0;
+    auto go = [&](auto elems, auto layer, auto bias, auto scale, auto post) {
+        auto kernel = residual_bwd_kernel<T, R, elems.value, layer.value, bias.value, scale.value, post.value>;
+        const int parts = (int)parts_for(a.rows, sets, p, resident_blocks(kernel, p.threads, smem));
+        blocks = (unsigned)(sets * parts);
+        kernel<<<blocks, p.threads, smem, st>>>(a, p.tpr, p.rows_at_once, parts);
     };
     const std::true_type yes;
     const std::false_type no;
-    auto post = [&](auto l, auto b, auto s) { a.post ? go(l, b, s, yes) : go(l, b, s, no); };
-    auto scale = [&](auto l, auto b) { a.scale ? post(l, b, yes) : post(l, b, no); };
-    auto bias = [&](auto l) { a.bias ? scale(l, yes) : scale(l, no); };
-    a.layer ? bias(yes) : bias(no);
-    cudaError_t e = cudaGetLastError();
-    const float *part = a.parts;
-    const size_t kind = (size_t)blocks * a.dim;
-    auto sum = [&](float *out, int64_t n) {   // n sets of rows, or all of them together
-        if (e == cudaSuccess)
-            e = launch_part_sum(part, n, (int)(blocks / n), a.dim, out, st);
-        part += kind;
+    auto post = [&](auto n, auto l, auto b, auto s) { a.post ? go(n, l, b, s, yes) : go(n, l, b, s, no); };
+    auto scale = [&](auto n, auto l, auto b) { a.scale ? post(n, l, b, yes) : post(n, l, b, no); };
+    auto bias = [&](auto n, auto l) { a.bias ? scale(n, l, yes) : scale(n, l, no); };
+    auto layer = [&](auto n) { a.layer ? bias(n, yes) : bias(n, no); };
+    p.elems == 8 ? layer(std::integral_constant<int, 8>()) : layer(std::integral_constant<int, 16>());
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    PartSum sums[kMaxSums];
+    int n = 0;
+    auto sum = [&](float *out, int64_t of) {   // per set of rows, or over all of them
+        sums[n] = PartSum{a.parts + (size_t)n * blocks * a.dim, out, of, (int)(blocks / of)};
+        n++;
     };
     sum(a.dweight, 1);
     if (a.bias)
@@ -392,7 +406,7 @@ template <typename T, typename R> cudaError_t bwd_typed(const ResidualArgs &a, c
         sum(a.dscale, sets);
     if (a.post)
         sum(a.dpost, 1);
-    return e;
+    return launch_part_sums(sums, n, a.dim, st);
 }
 
 }  // namespace
@@ -401,7 +415,8 @@ size_t residual_bwd_workspace(int64_t rows, int64_t samples, int dim, bool has_b
 {
     const int64_t sets = row_sets(samples, has_scale);
     const size_t kinds = 1 + has_bias + has_scale + has_post;
-    return kinds * (size_t)sets * residual_plan(rows, sets, dim).parts * dim * sizeof(float);
+    const NormPlan p = norm_threads(dim);
+    return kinds * (size_t)sets * parts_for(rows, sets, p, (int64_t)kSMs * (2048 / p.threads)) * dim * sizeof(float);
 }
 
 cudaError_t launch_residual_fwd(const ResidualArgs &a, cudaStream_t st)
