@@ -25,7 +25,9 @@ int64_t parts_for(int64_t rows, int64_t groups, const NormPlan &p, int64_t most)
     return share < 1 ? 1 : need < share ? need : share;
 }
 
-template <typename T, int ELEMS, bool BWD>
+// GATE: 0 none, 1 before the norm, 2 after it (a variant each: tests of it for
+// every element cost more than the arithmetic they choose).
+template <typename T, int ELEMS, int GATE, bool BWD>
 __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int tpr, int rpb, int parts)
 {
     constexpr int E = Vec<T>::N, NV = ELEMS / E;
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
         const bool live = r0 + sub < a.rows;
         const int64_t base = live ? (r0 + sub) * a.dim + col : 0;
         xr.load(x + base, lane_r, tpr, in, live);
-        if (z)
+        if (GATE)
             zr.load(z + base, lane_r, tpr, in, live);
         if (BWD)
             dr.load(dout + base, lane_r, tpr, in, live);
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
         const int64_t base = (r0 + sub) * a.dim + col;
         float xv[NV][E], zv[NV][E], dv[NV][E];
         xr.get(xv);
-        if (z)
+        if (GATE)
             zr.get(zv);
         if (BWD)
             dr.get(dv);
@@ -81,14 +83,12 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
         for (int v = 0; v < NV; v++)
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                sg[v][e] = z ? sigmoid_f(zv[v][e]) : 1.f;
-                const float s = z ? zv[v][e] * sg[v][e] : 1.f;
-                const float u = a.norm_first ? xv[v][e] : xv[v][e] * s;
+                sg[v][e] = GATE ? sigmoid_f(zv[v][e]) : 1.f;
+                const float s = GATE ? zv[v][e] * sg[v][e] : 1.f;
+                const float u = GATE == 1 ? xv[v][e] * s : xv[v][e];
                 sum[0] = fmaf(u, u, sum[0]);
-                if (BWD) {
-                    const float dn = a.norm_first ? dv[v][e] * s * w[v][e] : dv[v][e] * w[v][e];
-                    sum[1] = fmaf(dn, u, sum[1]);
-                }
+                if (BWD)
+                    sum[1] = fmaf((GATE == 2 ? dv[v][e] * s : dv[v][e]) * w[v][e], u, sum[1]);
             }
         if (BWD) {
             row_sum<2>(sum, tpr, red, turn);
@@ -105,22 +105,22 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
             float o[E], oz[E];
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                const float zz = zv[v][e], s = z ? zz * sg[v][e] : 1.f;
-                const float u = a.norm_first ? xv[v][e] : xv[v][e] * s, n = u * r;
+                const float zz = GATE ? zv[v][e] : 0.f, s = GATE ? zz * sg[v][e] : 1.f;
+                const float n = (GATE == 1 ? xv[v][e] * s : xv[v][e]) * r;
                 if (!BWD) {
-                    o[e] = a.norm_first ? n * w[v][e] * s : n * w[v][e];
+                    o[e] = GATE == 2 ? n * w[v][e] * s : n * w[v][e];
                 } else {
-                    const float ds = sg[v][e] * fmaf(zz, 1.f - sg[v][e], 1.f);
-                    const float dy = a.norm_first ? dv[v][e] * s : dv[v][e];
+                    const float ds = GATE ? sg[v][e] * fmaf(zz, 1.f - sg[v][e], 1.f) : 0.f;
+                    const float dy = GATE == 2 ? dv[v][e] * s : dv[v][e];
                     dw[v][e] = fmaf(dy, n, dw[v][e]);
                     const float du = r * fmaf(-n, m, dy * w[v][e]);
-                    o[e] = a.norm_first ? du : du * s;
-                    oz[e] = (a.norm_first ? dv[v][e] * n * w[v][e] : du * xv[v][e]) * ds;
+                    o[e] = GATE == 1 ? du * s : du;
+                    oz[e] = (GATE == 2 ? dv[v][e] * n * w[v][e] : du * xv[v][e]) * ds;
                 }
             }
             if (live && in[v]) {
                 store_row<T, E>(static_cast<T *>(BWD ? a.dx : a.out) + at, o);
-                if (BWD && z)
+                if (BWD && GATE)
                     store_row<T, E>(static_cast<T *>(a.dz) + at, oz);
             }
         }
@@ -156,7 +156,12 @@ template <typename T, bool BWD> cudaError_t launch_typed(const GatedArgs &a, cud
         *parts = (int)parts_for(a.rows, G, p, resident_blocks(kernel, p.threads, smem));
         kernel<<<(unsigned)(*parts * G), p.threads, smem, st>>>(a, p.tpr, p.rows_at_once, *parts);
     };
-    p.elems == 8 ? go(gated_norm_kernel<T, 8, BWD>) : go(gated_norm_kernel<T, 16, BWD>);
+    if (!a.z)
+        p.elems == 8 ? go(gated_norm_kernel<T, 8, 0, BWD>) : go(gated_norm_kernel<T, 16, 0, BWD>);
+    else if (!a.norm_first)
+        p.elems == 8 ? go(gated_norm_kernel<T, 8, 1, BWD>) : go(gated_norm_kernel<T, 16, 1, BWD>);
+    else
+        p.elems == 8 ? go(gated_norm_kernel<T, 8, 2, BWD>) : go(gated_norm_kernel<T, 16, 2, BWD>);
     return cudaGetLastError();
 }
 

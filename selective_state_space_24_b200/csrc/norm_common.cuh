@@ -63,13 +63,17 @@ template <typename R, int NV, int N> struct Raw {
                               ? reinterpret_cast<const uint4 *>(p + (lane_r + v * tpr) * N)[k]
                               : make_uint4(0, 0, 0, 0);
     }
+    __device__ __forceinline__ void get(int v, float (&f)[N]) const
+    {
+#pragma unroll
+        for (int k = 0; k < W; k++)
+            Vec<R>::unpack(w[v][k], &f[k * Vec<R>::N]);
+    }
     __device__ __forceinline__ void get(float (&f)[NV][N]) const
     {
 #pragma unroll
         for (int v = 0; v < NV; v++)
-#pragma unroll
-            for (int k = 0; k < W; k++)
-                Vec<R>::unpack(w[v][k], &f[v][k * Vec<R>::N]);
+            get(v, f[v]);
     }
 };
 template <typename R, int N> __device__ __forceinline__ void store_row(R *p, const float (&f)[N])
@@ -113,41 +117,40 @@ template <int N> __device__ __forceinline__ void load_f32(const float *p, float 
         f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
     }
 }
-constexpr int kRedMax = 2;   // values summed at once
+constexpr int kRedMax = 4;   // values summed at once
 // shared memory of row_sum: two buffers in turn, so that one barrier per sum
 // is enough (a buffer is written again only after the next sum's barrier)
-struct RedSmem {
-    float v[2][32][kRedMax];
+struct __align__(16) RedSmem {
+    float v[2][kRedMax][32];   // one value per warp
 };
 
 // Sums v[0..K) over the `tpr` neighbouring threads of this thread's row (a
 // power of two) -- each of them gets the same sums, added in the same order.
 // With more than 32 threads per row every thread of the block must call it.
-template <int K> __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, RedSmem &sm, int &turn)
+template <int K, int M> __device__ __forceinline__ void row_sum(float (&v)[M], int tpr, RedSmem &sm, int &turn)
 {
-    static_assert(K <= kRedMax, "");
+    static_assert(K <= kRedMax && K <= M, "the first K of M values");
     const int in_warp = tpr < 32 ? tpr : 32;
     for (int o = in_warp >> 1; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < K; k++)
             v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (tpr > 32) {
-        const int nw = tpr >> 5, lane = threadIdx.x & 31, w0 = (threadIdx.x / tpr) * nw;
-        if (lane == 0)
+    if (tpr > 32) {   // 2 to 16 warps a row: every thread adds their values itself
+        const int nw = tpr >> 5, w0 = (threadIdx.x / tpr) * nw;
+        if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int k = 0; k < K; k++)
-                sm.v[turn][threadIdx.x >> 5][k] = v[k];
+                sm.v[turn][k][threadIdx.x >> 5] = v[k];
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < K; k++)
-            v[k] = lane < nw ? sm.v[turn][w0 + lane][k] : 0.f;
-        for (int o = nw >> 1; o > 0; o >>= 1)
-#pragma unroll
-            for (int k = 0; k < K; k++)
-                v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-#pragma unroll
-        for (int k = 0; k < K; k++)
-            v[k] = __shfl_sync(0xffffffffu, v[k], 0);
+        for (int k = 0; k < K; k++) {
+            const float2 a = *reinterpret_cast<const float2 *>(&sm.v[turn][k][w0]);
+            v[k] = a.x + a.y;
+            for (int i = 2; i < nw; i += 2) {
+                const float2 b = *reinterpret_cast<const float2 *>(&sm.v[turn][k][w0 + i]);
+                v[k] += b.x + b.y;
+            }
+        }
         turn ^= 1;
     }
 }

@@ -223,10 +223,10 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
     for (int64_t r0 = set * per + (int64_t)part * rpb; r0 < row_end; r0 += stride) {
         const int64_t row = r0 + sub;
         const bool live = row < row_end;
-        float y[NV][E], g[NV][E];   // the stream (then its norm), dout (then dr)
+        float y[NV][E], g[NV][E];   // the stream (then its norm), dout weight (then dr)
         float d[NV][E], t[NV][E];   // the gradient of the stream's later uses, x
+        const Raw<T, NV, E> gc = gr;
         yr.get(y);
-        gr.get(g);
 #pragma unroll
         for (int v = 0; v < NV; v++)
 #pragma unroll
@@ -238,26 +238,70 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
             xr.get(t);
         if (r0 + stride < row_end)
             fetch(r0 + stride);
-        const float k = norm_stats<LAYER>(y, in, inv, a.eps, tpr, red, turn);
-        float s[2] = {0.f, 0.f};   // sums of g y and g
+        // the sums that need nothing else go together: of r^2 (of r, then of
+        // its centred squares), of g r, g and x^2
+        float sx = 0.f;
+        if (POST)
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    sx = fmaf(t[v][e], t[v][e], sx);
+        if (LAYER) {
+            float m[2] = {0.f, sx};
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    m[0] += y[v][e];
+            row_sum<2>(m, tpr, red, turn);
+            sx = m[1];
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    y[v][e] = in[v] ? y[v][e] - m[0] * inv : 0.f;
+        }
+        float s[4] = {0.f, 0.f, LAYER ? 0.f : sx, 0.f};
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            gc.get(v, g[v]);
+            float w[E];
+#pragma unroll
+            for (int e = 0; e < E; e++)
+                w[e] = 0.f;
+            if (in[v])
+                load_f32<E>(a.weight + (lane_r + v * tpr) * E, w);
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                g[v][e] *= w[e];
+                s[0] = fmaf(y[v][e], y[v][e], s[0]);
+                s[1] = fmaf(g[v][e], y[v][e], s[1]);
+                if (LAYER) {
+                    s[2] += y[v][e];   // the rounded mean's error, as in norm_stats
+                    s[3] += g[v][e];
+                }
+            }
+        }
+        row_sum<LAYER ? 4 : 3>(s, tpr, red, turn);
+        if (!LAYER)
+            sx = s[2];
+        const float off = LAYER ? s[2] * inv : 0.f, mg = LAYER ? s[3] * inv : 0.f;
+        const float k = rsqrtf(fmaf(-off, off, s[0] * inv) + a.eps);
+        const float mgy = k * (s[1] * inv - off * mg);   // mean(g y)
 #pragma unroll
         for (int v = 0; v < NV; v++)
             if (in[v]) {
-                float w[E];
-                load_f32<E>(a.weight + (lane_r + v * tpr) * E, w);
+                float o[E];   // dout
+                gc.get(v, o);
 #pragma unroll
                 for (int e = 0; e < E; e++) {
-                    y[v][e] *= k;
-                    dw[v][e] = fmaf(g[v][e], y[v][e], dw[v][e]);
+                    y[v][e] = (y[v][e] - off) * k;
+                    dw[v][e] = fmaf(o[e], y[v][e], dw[v][e]);
                     if (BIAS)
-                        db[v][e] += g[v][e];
-                    g[v][e] *= w[e];
-                    s[0] = fmaf(g[v][e], y[v][e], s[0]);
-                    s[1] += g[v][e];
+                        db[v][e] += o[e];
                 }
             }
-        row_sum<2>(s, tpr, red, turn);
-        const float mgy = s[0] * inv, mg = LAYER ? s[1] * inv : 0.f;
 #pragma unroll
         for (int v = 0; v < NV; v++)
             if (live && in[v]) {
@@ -272,17 +316,7 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
                     store_row<R, E>(static_cast<R *>(a.dres) + at, o);
             }
         if (SCALE || POST) {
-            float p = 1.f;
-            if (POST) {
-                float q[1] = {0.f};
-#pragma unroll
-                for (int v = 0; v < NV; v++)
-#pragma unroll
-                    for (int e = 0; e < E; e++)
-                        q[0] = fmaf(t[v][e], t[v][e], q[0]);
-                row_sum<1>(q, tpr, red, turn);
-                p = rsqrtf(q[0] * inv + a.eps);
-            }
+            const float p = POST ? rsqrtf(sx * inv + a.eps) : 1.f;
             float se[1] = {0.f};   // sum of e x p
 #pragma unroll
             for (int v = 0; v < NV; v++)
