@@ -121,7 +121,7 @@ __device__ __forceinline__ void mm(float (&acc)[MT][NT][4], int m0, int n0, int 
 #pragma unroll
                     for (int e = 0; e < 4; e++)
                         other[s][m * kApart][n * kApart][e] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < kdim; k += 8) {
         uint32_t ah[MT][4], al[MT][4], bh[NT][2], bl[NT][2];
 #pragma unroll
@@ -235,6 +235,22 @@ template <int ROWS, int N> __device__ __forceinline__ void load_f(float *dst, co
         const int r = x / Q, c = (x % Q) * 4;
         const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * pitch + c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + (size_t)r * N + c) : "memory");
+    }
+}
+// 64 rows of `kSlice` floats, ld apart, and the four scalars of every step
+__device__ __forceinline__ void load_slice(float *dst, const float *src, int ld)
+{
+    for (int x = threadIdx.x; x < kC * kSlice / 4; x += kThreads) {
+        const int r = x / (kSlice / 4), c = (x % (kSlice / 4)) * 4;
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * (kSlice + 8) + c);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + (size_t)r * ld + c) : "memory");
+    }
+}
+__device__ __forceinline__ void load_scalars(float *dst, const float *src)
+{
+    if (threadIdx.x < kC) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + 4 * threadIdx.x);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + 4 * threadIdx.x) : "memory");
     }
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -424,6 +440,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
 template <int K> struct ChainSmem {
     float w[2][kC * pf(K)];
     bf16 k[2][kC * ph(K)];
+    float u[2][kC * (kSlice + 8)], v[2][4 * kC];   // U; cs, b, 1 / |k|, scale / |q|
     float s[kSlice * pf(K)], n[kC * (kSlice + 8)];
 };
 template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const GdrArgs a, const Layout lay)
@@ -440,6 +457,8 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
             const Where w = where(a, bh, n);
             load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pf(K));
             load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+            load_slice(s.u[n & 1], base + lay.base(bh, n) + lay.U() + v0, a.V);
+            load_scalars(s.v[n & 1], base + lay.base(bh, n));
         }
         cp_commit();
     };
@@ -451,14 +470,10 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
     for (int n = 0; n < lay.NC; n++) {
         float *ws = base + lay.base(bh, n);
         fetch(n + 1);
-        float u[1][2][4];   // this thread's part of U, and the factors of its rows of N
-        pairs(u, mN, nN, [&](int i, int j, float &x, float &y) {
-            const float2 f = *reinterpret_cast<const float2 *>(ws + lay.U() + i * a.V + v0 + j);
-            x = f.x, y = f.y;
-        });
-        const float end = ws[lay.cs() + kC - 1];
         cp_wait<1>();
         __syncthreads();
+        const float *u = s.u[n & 1], *cs = s.v[n & 1], *rk = cs + 2 * kC;
+        const float end = cs[kC - 1];
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.S0() + (size_t)v0 * K + x) =
                 *reinterpret_cast<const float4 *>(&s.s[(x / K) * pf(K) + x % K]);
@@ -470,14 +485,10 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
                        [&](int k, int j) { return s.s[j * pf(K) + k]; });
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
-            const float e[2] = {ws[lay.rk() + i0] * ex2_mufu(end - ws[lay.cs() + i0]),
-                                ws[lay.rk() + i0 + 8] * ex2_mufu(end - ws[lay.cs() + i0 + 8])};
-#pragma unroll
-            for (int q = 0; q < 2; q++)
-#pragma unroll
-                for (int x = 0; x < 4; x++)
-                    acc[0][q][x] = u[0][q][x] - acc[0][q][x];
+            const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
+                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * pn + j]);
+                x = f2.x - x, y = f2.y - y;
                 st2(ws + lay.U() + i * a.V + v0 + j, x, y);
                 const float f = e[(i - i0) >> 3];
                 st2(&s.n[i * pn + j], x * f, y * f);
@@ -501,6 +512,7 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
 template <int K> struct ReverseSmem {
     float w[2][kC * pf(K)];
     bf16 k[2][kC * ph(K)], q[2][kC * ph(K)], o[2][kC * ph(kSlice)];
+    float u[2][kC * (kSlice + 8)], v[2][4 * kC];   // P^T dO; scalars
     float g[kSlice * pf(K)], n[kC * (kSlice + 8)];
     float f[kC];
 };
@@ -522,6 +534,8 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
             load_rows<K>(s.q[n & 1], static_cast<const bf16 *>(a.q) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
             load_rows<kSlice>(s.o[n & 1], static_cast<const bf16 *>(ga.dout) + (w.tok * a.Hv + w.h) * a.V + v0,
                               (size_t)a.Hv * a.V, w.valid);
+            load_slice(s.u[n & 1], base + lay.base(bh, n) + lay.dN() + v0, a.V);
+            load_scalars(s.v[n & 1], base + lay.base(bh, n));
         }
         cp_commit();
     };
@@ -533,16 +547,12 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
     for (int n = lay.NC - 1; n >= 0; n--) {
         float *ws = base + lay.base(bh, n);
         fetch(n - 1);
-        float u[1][2][4];
-        pairs(u, mN, nN, [&](int i, int j, float &x, float &y) {
-            const float2 f = *reinterpret_cast<const float2 *>(ws + lay.dN() + i * a.V + v0 + j);
-            x = f.x, y = f.y;
-        });
-        const float end = ws[lay.cs() + kC - 1];
-        if (threadIdx.x < kC)
-            s.f[threadIdx.x] = ws[lay.rq() + threadIdx.x] * ex2_mufu(ws[lay.cs() + threadIdx.x]);
         cp_wait<1>();
         __syncthreads();
+        const float *u = s.u[n & 1], *cs = s.v[n & 1], *rk = cs + 2 * kC, *rq = cs + 3 * kC;
+        const float end = cs[kC - 1];
+        if (threadIdx.x < kC)
+            s.f[threadIdx.x] = rq[threadIdx.x] * ex2_mufu(cs[threadIdx.x]);
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.dS() + (size_t)v0 * K + x) =
                 *reinterpret_cast<const float4 *>(&s.g[(x / K) * pf(K) + x % K]);
@@ -554,14 +564,11 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
                          [&](int k, int j) { return s.g[j * pf(K) + k]; });
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
-            const float e[2] = {ws[lay.rk() + i0] * ex2_mufu(end - ws[lay.cs() + i0]),
-                                ws[lay.rk() + i0 + 8] * ex2_mufu(end - ws[lay.cs() + i0 + 8])};
-#pragma unroll
-            for (int q = 0; q < 2; q++)
-#pragma unroll
-                for (int x = 0; x < 4; x++)
-                    acc[0][q][x] = fmaf(e[x >> 1], acc[0][q][x], u[0][q][x]);
+            const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
+                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * pn + j]);
+                const float f = e[(i - i0) >> 3];
+                x = fmaf(f, x, f2.x), y = fmaf(f, y, f2.y);
                 st2(ws + lay.dN() + i * a.V + v0 + j, x, y);
                 st2(&s.n[i * pn + j], -x, -y);
             });
