@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar_init(&bars.scal[i], 32);
         for (int i = 0; i < 2; i++) {
             bar_init(&bars.vfull[i], 1);
-            bar_init(&bars.out[i], 4);
+            bar_init(&bars.out[i], kStateWarps);
             bar_init(&bars.ready[i], 4);
             bar_init(&bars.kk[i], 1);
             bar_init(&bars.o[i], 1);
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&bars.t, 1);
         bar_init(&bars.n, kStateWarps);
         bar_init(&bars.qs, 1);
-        bar_init(&bars.oread, 4);
+        bar_init(&bars.oread, kStateWarps);
         bar_init(&bars.kkread, 4);
         bar_init(&bars.done, 1);
         bars.abort = 0;
@@ -199,8 +199,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_before();
         arrive1(&bars.s[half]);
+        // outputs of a quarter of chunk c's steps, in the place of its V
+        auto outputs = [&](int c) {
+            if (!wait(&bars.o[c & 1], phase2(c)))
+                return false;
+            fence_after();
+            if (live) {
+                const Vec *ve = vec(c);
+                const uint32_t vpitch = 2 * V;
+                uint8_t *ot = vtile(c) + 16 * quarter * vpitch + 2 * v;
+                uint32_t q[16], p[16];
+                tmem_ld(tl + kColQS + 16 * quarter, q);
+                tmem_ld(tl + kColPN + 16 * quarter, p);
+                tmem_wait(q);
+                tmem_wait(p);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float2 g = *reinterpret_cast<const float2 *>(&ve->gq[16 * quarter + e]);
+                    const float2 y = __ffma2_rn(g, make_float2(__uint_as_float(q[e]), __uint_as_float(q[e + 1])),
+                                                make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])));
+                    const uint32_t w = pack(y.x, y.y);
+                    *reinterpret_cast<uint16_t *>(ot + e * vpitch) = (uint16_t)w;
+                    *reinterpret_cast<uint16_t *>(ot + (e + 1) * vpitch) = (uint16_t)(w >> 16);
+                }
+            }
+            fence_before();
+            arrive1(&bars.oread);
+            fence_smem();
+            arrive1(&bars.out[c & 1]);
+            return true;
+        };
+        bool ok = true;
         for (int c = 0; c < nch; c++) {
             const Vec *ve = vec(c);
+            ok = false;
             // 1. diag(b)(V - diag(c) K^ S^T), this half's 32 steps
             if (!wait(&bars.vfull[c & 1], phase2(c)) || !wait(&bars.ready[c & 1], phase2(c)) || !wait(&bars.ks, c & 1))
                 break;
@@ -227,8 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_before();
             arrive1(&bars.d);
-            // 2. N for the outputs, N diag(e) for the state
-            if (!wait(&bars.t, c & 1))
+            // 2. N for the outputs, N diag(e) for the state (the last chunk's outputs
+            // while T's product runs)
+            if ((c > 0 && !outputs(c - 1)) || !wait(&bars.t, c & 1))
                 break;
             fence_after();
             if (live) {
@@ -277,7 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_before();
             arrive1(&bars.s[half]);
+            ok = true;
         }
+        if (ok && nch > 0)
+            outputs(nch - 1);
         if (live && a.last && !*abort) {
 #pragma unroll
             for (int i = 0; i < KQ; i += 4)
@@ -291,43 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool isq = pw >= 2;
         const int i = row & 63;                  // step in the chunk
         const uint32_t tl = tm + ((uint32_t)(pw * 32) << 16);
-        // outputs of chunk c (lane = value channel), in the place of its V
-        auto outputs = [&](int c) {
-            if (!wait(&bars.o[c & 1], phase2(c)))
-                return false;
-            fence_after();
-            if (pw * 32 < V) {
-                const Vec *ve = vec(c);
-                const uint32_t vpitch = 2 * V;
-                uint8_t *ot = vtile(c) + 2 * row;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    uint32_t q[16], p[16];
-                    tmem_ld(tl + kColQS + 16 * j, q);
-                    tmem_ld(tl + kColPN + 16 * j, p);
-                    tmem_wait(q);
-                    tmem_wait(p);
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float2 g = *reinterpret_cast<const float2 *>(&ve->gq[16 * j + e]);
-                        const float2 y = __ffma2_rn(g, make_float2(__uint_as_float(q[e]), __uint_as_float(q[e + 1])),
-                                                    make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])));
-                        const uint32_t w = pack(y.x, y.y);
-                        *reinterpret_cast<uint16_t *>(ot + (16 * j + e) * vpitch) = (uint16_t)w;
-                        *reinterpret_cast<uint16_t *>(ot + (16 * j + e + 1) * vpitch) = (uint16_t)(w >> 16);
-                    }
-                }
-            }
-            fence_before();
-            arrive1(&bars.oread);
-            fence_smem();
-            arrive1(&bars.out[c & 1]);
-            return true;
-        };
-        int turn = 0, c = team;
-        bool ok = true;
-        for (; c < nch; c += 2, turn++) {
-            ok = false;
+        int turn = 0;
+        for (int c = team; c < nch; c += 2, turn++) {
             Vec *ve = vec(c);
             const uint8_t *st = stage(c);
             uint8_t *Pb = sm + kOffP + (c % kP) * 2 * kTile, *Tb = sm + kOffT + team * 2 * kTile;
@@ -367,8 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ve->gq[i] = 1.f;
             }
             arrive1(&bars.team[team][0]);
-            if (c >= 2 && !outputs(c - 2))   // before its products take tensor memory back
-                break;
             if (!wait(&bars.team[team][0], turn & 1) || !wait(&bars.kk[team], turn & 1))
                 break;
             fence_after();
@@ -528,10 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
             fence_smem();
             arrive1(&bars.ready[team]);
-            ok = true;
         }
-        if (ok && c >= 2)   // c - 2: this team's last chunk
-            outputs(c - 2);
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
     if (warp == kMmaWarp) {
