@@ -58,7 +58,7 @@ constexpr int kOffP = kOffV + 2 * 2 * kTile;
 constexpr int kOffT = kOffP + kP * 2 * kTile;
 constexpr int kOffVec = kOffT + 2 * 2 * kTile;
 struct Vec {               // of one chunk
-    float2 csk[kC];        // cs, 1 / |k|
+    float ncs[kC], rk[kC]; // -cs, 1 / |k| (apart: neighbours make pairs for packed arithmetic)
     float4 bg[kC / 2];     // b of two steps, their -b c / |k|
     float gq[kC];          // c scale / |q| (first 1 / |q|)
     float ek[kC];          // e / |k|
@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float n0 = rsqrtf(((lane >> 2) & 1 ? acc[0][1] : acc[0][0]) + kL2Eps);
                         const float n1 = rsqrtf(((lane >> 2) & 1 ? acc[1][3] : acc[1][2]) + kL2Eps);
                         if (m == 0) {
-                            ve->csk[r0].y = n0;
-                            ve->csk[r0 + 8].y = n1;
+                            ve->rk[r0] = n0;
+                            ve->rk[r0 + 8] = n1;
                         } else {
                             ve->gq[r0] = n0;
                             ve->gq[r0 + 8] = n1;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             } else if (!isq) {
-                ve->csk[i].y = 1.f;
+                ve->rk[i] = 1.f;
             } else {
                 ve->gq[i] = 1.f;
             }
@@ -371,8 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(&bars.team[team][0], turn & 1) || !wait(&bars.kk[team], turn & 1))
                 break;
             fence_after();
-            const float2 own = ve->csk[i];
-            const float csi = own.x, f = isq ? a.scale * ve->gq[i] : own.y * ve->b[i];   // the row's factor
+            const float csi = -ve->ncs[i], f = isq ? a.scale * ve->gq[i] : ve->rk[i] * ve->b[i];   // the row's factor
             const int last = isq ? i : i - 1, blk = i >> 4, il = i & 15;
             // rows of 16 as bf16 pairs: of P; of A left of the diagonal block, that block's inverse in it
             auto put = [&](uint8_t *to, int at_blk, const float (&x)[16]) {
@@ -399,13 +398,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld(tl + kColKK + 16 * p, r);
                 tmem_wait(r);
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const float4 ck = *reinterpret_cast<const float4 *>(&ve->csk[16 * p + j]);
-                    const float2 e = __fadd2_rn(make_float2(csi, csi), make_float2(-ck.x, -ck.z));
-                    const float2 g = __fmul2_rn(make_float2(ex2_mufu(e.x), ex2_mufu(e.y)), make_float2(ck.y * f, ck.w * f));
-                    const float2 x = __fmul2_rn(g, make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])));
-                    w[j] = x.x;
-                    w[j + 1] = x.y;
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 nc = *reinterpret_cast<const float4 *>(&ve->ncs[16 * p + j]);
+                    const float4 rk = *reinterpret_cast<const float4 *>(&ve->rk[16 * p + j]);
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const float2 e = __fadd2_rn(make_float2(csi, csi), h ? make_float2(nc.z, nc.w) : make_float2(nc.x, nc.y));
+                        const float2 g = __fmul2_rn(make_float2(ex2_mufu(e.x), ex2_mufu(e.y)),
+                                                    h ? make_float2(rk.z, rk.w) : make_float2(rk.x, rk.y));
+                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(r[j + 2 * h]), __uint_as_float(r[j + 2 * h + 1])),
+                                                    make_float2(f, f));
+                        const float2 y = __fmul2_rn(g, x);
+                        w[j + 2 * h] = y.x;
+                        w[j + 2 * h + 1] = y.y;
+                    }
                 }
                 if (p >= reach - 1) {   // the warp's diagonal: zeros right of it
                     const int n = last - 16 * p;
@@ -491,16 +497,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             if (pw == 0) {   // no blocks left of the first: the scalars instead
-                const float end = ve->csk[kC - 1].x;
+                const float end = -ve->ncs[kC - 1];
 #pragma unroll
                 for (int s = 0; s < 2; s++) {
                     const int at = lane + 32 * s;
-                    const float2 ck = ve->csk[at];
-                    const float bb = ve->b[at], cd = ex2_mufu(ck.x);
+                    const float nc = ve->ncs[at], rk = ve->rk[at], bb = ve->b[at];
                     float *bg = reinterpret_cast<float *>(&ve->bg[at / 2]) + (at & 1);
                     bg[0] = bb;
-                    bg[2] = -bb * cd * ck.y;
-                    ve->ek[at] = ex2_mufu(end - ck.x) * ck.y;
+                    bg[2] = -bb * ex2_mufu(-nc) * rk;
+                    ve->ek[at] = ex2_mufu(end + nc) * rk;
                 }
                 if (lane == 0)
                     ve->dec = ex2_mufu(end);
@@ -709,8 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             issued = c;
             Vec *ve = vec(c);
-            ve->csk[2 * lane].x = incl - g[1];
-            ve->csk[2 * lane + 1].x = incl;
+            ve->ncs[2 * lane] = g[1] - incl;
+            ve->ncs[2 * lane + 1] = -incl;
             ve->b[2 * lane] = bb[0];
             ve->b[2 * lane + 1] = bb[1];
             bar_arrive(&bars.scal[c % kVecs]);
