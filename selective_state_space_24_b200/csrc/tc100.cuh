@@ -30,18 +30,19 @@ __device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity)
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile("{.reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
                  : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "r"(bar), "r"(parity)
                  : "memory");
     return ok;
 }
+__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity) { return bar_test(smem_u32(bar), parity); }
 
-constexpr long kWaitLimit = 1l << 20;    // polls of a pipeline wait
-constexpr long kDrainLimit = 1l << 22;   // polls of a wait for this block's own copies and products
+constexpr int kWaitLimit = 1 << 20;    // polls of a pipeline wait
+constexpr int kDrainLimit = 1 << 22;   // polls of a wait for this block's own copies and products
 
 // Bounded wait of a whole warp.  On giving up a thread sets *error (the
 // library's word, read by ssm_check_device) and the block's abort word, and
@@ -49,26 +50,23 @@ constexpr long kDrainLimit = 1l << 22;   // polls of a wait for this block's own
 // with wrong values, and says so.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *error)
 {
-    bool ok = false;
-    for (long it = 0; it < kWaitLimit; it++) {
-        if (bar_test(bar, parity)) {
-            ok = true;
-            break;
-        }
-        if ((it & 255) == 255 && *abort)
-            break;
+    const uint32_t b = smem_u32(bar);
+#pragma unroll 1
+    for (int it = 0; it < kWaitLimit; it++) {   // each test waits a while by itself
+        if (__all_sync(0xffffffffu, bar_test(b, parity)))
+            return true;
+        if ((it & 63) == 63 && __any_sync(0xffffffffu, *abort))
+            return false;
     }
-    if (!ok && !*abort) {
-        *abort = 1;
-        atomicExch(error, 1u);
-    }
-    return __all_sync(0xffffffffu, ok);
+    *abort = 1;
+    atomicExch(error, 1u);
+    return false;
 }
 // Wait at the end for work that completes by itself (loads landing, products
 // retiring); it ignores the abort word.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, unsigned *error)
 {
-    for (long it = 0; it < kDrainLimit; it++)
+    for (int it = 0; it < kDrainLimit; it++)
         if (bar_test(bar, parity))
             return;
     atomicExch(error, 1u);
