@@ -31,13 +31,15 @@
 // log decay's gradient keeps float32's precision: an operand is hi + lo, both
 // tf32 (11 bits each), and a product is hi hi + hi lo + lo hi; K, Q, V and dO
 // as they came are bf16 and exact in hi alone.  What only reaches bf16
-// results (dP, dA times K and Q) takes hi hi.  (Pairs of bf16 leave dA up to
+// results (dP, dA times K and Q) takes one tf32 part; K K^T and Q K^T are bf16
+// products.  (Pairs of bf16 leave dA up to
 // 3e-5 off where the terms cancel.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "gdr_math.cuh"
+#include "tc100.cuh"
 
 namespace ssm {
 namespace {
@@ -162,6 +164,37 @@ __device__ __forceinline__ void mm(float (&acc)[MT][NT][4], int m0, int n0, int 
 #pragma unroll
                 for (int e = 0; e < 4; e++)
                     acc[m][n][e] += other[0][m * kApart][n * kApart][e] + other[1][m * kApart][n * kApart][e];
+}
+// The same for bf16 tiles in shared memory (one part each), 16 of k at a time:
+// A[m][k] of pitch pa, B[n][k] of pitch pb; NT even.
+template <int MT, int NT>
+__device__ __forceinline__ void mm16(float (&acc)[MT][NT][4], int m0, int n0, int kdim, const bf16 *A, int pa, const bf16 *B,
+                                     int pb)
+{
+    const int lane = threadIdx.x & 31, r = lane & 7, q = lane >> 3;   // row of the 8 x 8 block q
+    const uint32_t a0 = tc::smem_u32(A), b0 = tc::smem_u32(B);
+#pragma unroll 2
+    for (int k = 0; k < kdim; k += 16) {
+        uint32_t a[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+            // blocks in the order (m, k), (m + 8, k), (m, k + 8), (m + 8, k + 8)
+            const int mm_ = m0 + 16 * m + 8 * (q & 1), kk = k + 8 * (q >> 1);
+            tc::ldsm(a0 + 2 * ((mm_ + r) * pa + kk), a[m]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            // (n, k), (n, k + 8), (n + 8, k), (n + 8, k + 8)
+            const int nn = n0 + 8 * n + 8 * (q >> 1), kk = k + 8 * (q & 1);
+            uint32_t b[4];
+            tc::ldsm(b0 + 2 * ((nn + r) * pb + kk), b);
+#pragma unroll
+            for (int m = 0; m < MT; m++) {
+                tc::mma16816(acc[m][n], a[m], b[0], b[1]);
+                tc::mma16816(acc[m][n + 1], a[m], b[2], b[3]);
+            }
+        }
+    }
 }
 template <int MT, int NT> __device__ __forceinline__ void zero(float (&acc)[MT][NT][4])
 {
@@ -341,9 +374,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
         float kk[2][2][4], qk[2][2][4];
         zero(kk);
         zero(qk);
-        auto krow = [&](int k, int j) { return bf(&s.k[j * ph(K) + k]); };
-        mm<kExact, kExact>(kk, m0, 16 * wn, K, [&](int i, int k) { return bf(&s.k[i * ph(K) + k]); }, krow);
-        mm<kExact, kExact>(qk, m0, 16 * wn, K, [&](int i, int k) { return bf(&s.q[i * ph(K) + k]); }, krow);
+        mm16(kk, m0, 16 * wn, K, s.k, ph(K), s.k, ph(K));
+        mm16(qk, m0, 16 * wn, K, s.q, ph(K), s.k, ph(K));
         each(kk, m0, 16 * wn, [&](int i, int j, float v) {
             s.a[i * kPX + j] = j < i ? s.b[i] * ex2_mufu(s.cs[i] - s.cs[j]) * s.rk[i] * s.rk[j] * v : 0.f;
             s.t[i * kPX + j] = 0.f;
@@ -696,9 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             float kk[2][2][4], qk[2][2][4];
             zero(kk);
             zero(qk);
-            auto krow = [&](int k, int j) { return Kt(j, k); };
-            mm<kExact, kExact>(kk, m0, nC, K, Kt, krow);
-            mm<kExact, kExact>(qk, m0, nC, K, Qt, krow);
+            mm16(kk, m0, nC, K, s.k, ph(K), s.k, ph(K));
+            mm16(qk, m0, nC, K, s.q, ph(K), s.k, ph(K));
 #pragma unroll
             for (int m = 0; m < 2; m++)
 #pragma unroll
