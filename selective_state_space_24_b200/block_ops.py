@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import SSMError, _dtype_code, _torch, capi
+from . import SSM_BF16, SSM_F32, SSMError, _torch, capi
 
 __all__ = ["gdr_chunk_fwd", "gdr_chunk_bwd", "gdr_step", "gated_norm_fwd", "gated_norm_bwd", "residual_norm_fwd",
            "residual_norm_bwd", "gdr_dims", "gdr_inputs", "gdr_grads", "norm_dims", "residual_norm_params",
@@ -68,28 +68,44 @@ SIGNATURES = {
 }
 
 
-def _raw_stream(torch, index):
-    """The handle of the device's current stream."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without building a Stream object
-    return torch.cuda.current_stream(index).cuda_stream if get is None else get(index)
+class _Torch:
+    """What every call needs of torch, looked up once."""
+    torch = None
+
+    @classmethod
+    def load(cls):
+        torch = _torch()
+        cls.codes = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+        cls.f32, cls.empty_like = torch.float32, torch.empty_like
+        cls.current_device = torch.cuda.current_device
+        # the handle of a device's current stream, without building a Stream object
+        cls.stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        cls.torch = torch
 
 
 class _Call:
     """One call's device, stream and temporaries."""
 
     def __init__(self, x, name, stream):
-        if not x.is_cuda:
+        if _Torch.torch is None:
+            _Torch.load()
+        self.index = x.get_device()
+        if self.index < 0:
             raise ValueError(f"{name}: tensors must be on a CUDA device")
-        self.torch = torch = _torch()
-        self.name, self.device, self.dtype, self.code = name, x.device, x.dtype, _dtype_code(x)
-        self.index, self.f32, self.stream = x.get_device(), torch.float32, stream
+        self.dtype = x.dtype
+        self.code = _Torch.codes.get(self.dtype)
+        if self.code is None:
+            raise TypeError(f"{name}: unsupported dtype {x.dtype}")
+        self.torch, self.f32 = _Torch.torch, _Torch.f32
+        self.name, self.device, self.stream = name, x.device, stream
         self.made = []   # allocated here, to be kept for a stream that is not the current one
 
     def ptr(self, t, what, shape, dtype):
         """The address of t after its checks (None for None)."""
         if t is None:
             return None
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.get_device() == self.index and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
             return t.data_ptr()
         if t.dtype != dtype:
             raise TypeError(f"{self.name}: {what} must be {dtype}, got {t.dtype}")
@@ -100,7 +116,7 @@ class _Call:
         raise ValueError(f"{self.name}: {what} must be contiguous")
 
     def like(self, t):
-        t = self.torch.empty_like(t)
+        t = _Torch.empty_like(t)
         self.made.append(t)
         return t
 
@@ -121,20 +137,18 @@ class _Call:
 
     def run(self, fn, *args):
         """fn(*args, stream) on the tensors' device; raises on an error."""
-        cuda = self.torch.cuda
-        if self.index != cuda.current_device():
-            with cuda.device(self.device):
+        if self.index != _Torch.current_device():
+            with self.torch.cuda.device(self.device):
                 return self._run(fn, args)
         return self._run(fn, args)
 
     def _run(self, fn, args):
-        if self.stream is None:
-            status = fn(*args, _raw_stream(self.torch, self.index))
-        else:
-            status = fn(*args, self.stream.cuda_stream)
-            if self.stream != self.torch.cuda.current_stream(self.index):
-                for t in self.made:
-                    t.record_stream(self.stream)
+        here = _Torch.stream(self.index)
+        s = here if self.stream is None else self.stream.cuda_stream
+        status = fn(*args, s)
+        if s != here:
+            for t in self.made:
+                t.record_stream(self.stream)
         if status != 0:
             raise SSMError(status, self.name)
 
