@@ -611,6 +611,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 commit(&bars.t);
             }
             __syncwarp();
+            // for the chunk after next, if its tiles are here (else further on):
+            // its team may overwrite T now, and has that much more time
+            kk_if_ready(c + 2);
             // Q~ S^T, once the last chunk's outputs are read; done before S makes way
             if (c > 0 && !wait(&bars.oread, (c - 1) & 1))
                 break;
