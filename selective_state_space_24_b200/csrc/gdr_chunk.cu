@@ -780,9 +780,27 @@ template <int K> cudaError_t launch(const GdrArgs &a, cudaStream_t st)
 
 size_t gdr_chunk_ws_bytes(const GdrArgs &) { return 0; }
 
+namespace {
+
+// Sequences this short go step by step: one chunk takes 16.5 us (K = 128; 11
+// us for K = 64) however little of it is filled, the recurrent kernel 2 us and
+// 0.54 us a step while its blocks (of 32 state rows) are at most one per SM,
+// 1.0 us a step with 3.5 of them, 0.8 us a step for K = 64.  Measured on B200,
+// chunked / recurrent: 32 heads L 24 16.7 / 15.1 us, L 32 16.7 / 19.6; 128
+// heads L 12 17.3 / 15.3, L 16 17.3 / 19.5; 1024 heads L 12 121 / 96, L 16
+// 121 / 124; K = V = 64, 32 heads L 8 10.9 / 8.1, L 12 10.9 / 11.6.
+int recurrent_limit(const GdrArgs &a)
+{
+    if (a.K == 64)
+        return 10;
+    return (int64_t)a.Bsz * a.Hv * (a.V / 32) <= 148 ? 26 : 14;
+}
+
+}  // namespace
+
 cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st)
 {
-    if (a.L < 16)
+    if (a.L <= recurrent_limit(a))
         return launch_gdr_recurrent(a, st);
     return a.K == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
