@@ -76,12 +76,11 @@ constexpr int kPX = kC + 4;
 
 __device__ __forceinline__ float bf(const bf16 *p) { return __bfloat162float(*p); }
 
-__device__ __forceinline__ uint32_t tf32(float x)
-{
-    uint32_t r;
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-    return r;
-}
+// tf32 keeps the upper 19 bits of a float32: cut off, or rounded.  (Integer
+// operations: the conversion instruction runs on the slow pipe and bounded
+// the products.)
+__device__ __forceinline__ uint32_t tf32_cut(float x) { return __float_as_uint(x) & 0xffffe000u; }
+__device__ __forceinline__ uint32_t tf32_round(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
 {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -97,7 +96,7 @@ template <Part P, int N> __device__ __forceinline__ void parts(const float (&x)[
 {
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        hi[i] = P == kExact ? __float_as_uint(x[i]) : tf32(x[i]);
+        hi[i] = P == kExact ? __float_as_uint(x[i]) : P == kOne ? tf32_round(x[i]) : tf32_cut(x[i]);
         lo[i] = P == kTwo ? __float_as_uint(x[i] - __uint_as_float(hi[i])) : 0u;
     }
 }
