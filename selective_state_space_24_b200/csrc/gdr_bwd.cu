@@ -627,7 +627,7 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
 template <int K, int V> struct GradSmem {
     bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(V)];
     float n[kC * pf(V)], r[kC * pf(V)], x[kC * kPX];
-    float m[kC * pf(K)];   // T first, then 64 rows of a state at a time
+    float t[kC * kPX], m[2][kSlice * pf(K)];   // T; 32 rows of a state, the next 32
     float cs[4 * kC];       // cs, b, rk, rq as in the workspace
     float dcs[kC], sum[6][4][kC], red[8];   // sum: row sums of each column of warps
 };
@@ -682,16 +682,25 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         load_rows<V>(s.o, static_cast<const bf16 *>(ga.dout) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid);
         load_f<kC, V>(s.n, ws + lay.U(), pf(V));
         load_f<kC, V>(s.r, ws + lay.dN(), pf(V));
-        load_f<kC, kC>(s.m, ws + lay.T(), kPX);
+        load_f<kC, kC>(s.t, ws + lay.T(), kPX);
         cp_commit();
-        cp_wait<0>();
+        // S0 and then dS1, 32 rows at a time, two pieces on their way
+        constexpr int kPieces = V / kSlice;
+        auto fetch = [&](int i) {
+            if (i < 2 * kPieces)
+                load_f<kSlice, K>(s.m[i & 1], (i < kPieces ? S0 : dS - (size_t)V * K) + (size_t)i * kSlice * K, pf(K));
+            cp_commit();
+        };
+        fetch(0);
+        fetch(1);
+        cp_wait<2>();
         __syncthreads();
         const float end = cs[kC - 1];
         // R' = T^T dN
         {
             float r[2][NV][4];
             zero(r);
-            mm<kTwo, kTwo>(r, m0, nV, kC, [&](int i, int k) { return s.m[k * kPX + i]; },
+            mm<kTwo, kTwo>(r, m0, nV, kC, [&](int i, int k) { return s.t[k * kPX + i]; },
                            [&](int k, int j) { return s.r[k * pf(V) + j]; });
             __syncthreads();
             float dbr[4] = {};
@@ -776,15 +785,16 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         float Y[2][NK][4], q[2][NK][4];
         zero(Y);
         zero(q);
-        for (int v0 = 0; v0 < V; v0 += 64) {
+        for (int i = 0; i < kPieces; i++) {
+            const int v0 = i * kSlice;
+            const float *St = s.m[i & 1];
+            cp_wait<1>();
             __syncthreads();
-            load_f<kC, K>(s.m, S0 + (size_t)v0 * K, pf(K));
-            cp_commit();
-            cp_wait<0>();
+            auto Sf = [&](int k, int j) { return St[k * pf(K) + j]; };
+            mm<kTwo, kTwo>(Y, m0, nK, kSlice, [&](int r, int k) { return s.r[r * pf(V) + v0 + k]; }, Sf);
+            mm<kExact, kTwo>(q, m0, nK, kSlice, [&](int r, int k) { return bf(&s.o[r * ph(V) + v0 + k]); }, Sf);
             __syncthreads();
-            auto St = [&](int k, int j) { return s.m[k * pf(K) + j]; };
-            mm<kTwo, kTwo>(Y, m0, nK, 64, [&](int i, int k) { return s.r[i * pf(V) + v0 + k]; }, St);
-            mm<kExact, kTwo>(q, m0, nK, 64, [&](int i, int k) { return bf(&s.o[i * ph(V) + v0 + k]); }, St);
+            fetch(i + 2);
         }
         {
             each(Y, m0, nK, [&](int i, int, float &v) { v *= -ex2_mufu(cs[i]); });
@@ -821,19 +831,20 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         zero(Y);
         float through = 0.f;
         const float dec = ex2_mufu(end);
-        for (int v0 = 0; v0 < V; v0 += 64) {
+        for (int i = kPieces; i < 2 * kPieces; i++) {
+            const int v0 = (i - kPieces) * kSlice;
+            const float *St = s.m[i & 1];
+            cp_wait<1>();
             __syncthreads();
-            load_f<kC, K>(s.m, dS + (size_t)v0 * K, pf(K));
-            cp_commit();
-            cp_wait<0>();
-            __syncthreads();
-            mm<kTwo, kTwo>(Y, m0, nK, 64, [&](int i, int k) { return s.n[i * pf(V) + v0 + k]; },
-                           [&](int k, int j) { return s.m[k * pf(K) + j]; });
-            for (int x = threadIdx.x * 4; x < 64 * K; x += kThreads * 4) {   // c_end <dS1, S0>
+            mm<kTwo, kTwo>(Y, m0, nK, kSlice, [&](int r, int k) { return s.n[r * pf(V) + v0 + k]; },
+                           [&](int k, int j) { return St[k * pf(K) + j]; });
+            for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4) {   // c_end <dS1, S0>
                 const float4 f = *reinterpret_cast<const float4 *>(S0 + (size_t)v0 * K + x);
-                const float4 d = *reinterpret_cast<const float4 *>(&s.m[(x / K) * pf(K) + x % K]);
+                const float4 d = *reinterpret_cast<const float4 *>(&St[(x / K) * pf(K) + x % K]);
                 through = fmaf(dec * d.x, f.x, fmaf(dec * d.y, f.y, fmaf(dec * d.z, f.z, fmaf(dec * d.w, f.w, through))));
             }
+            __syncthreads();
+            fetch(i + 2);
         }
         each(Y, m0, nK, [&](int i, int, float &v) { v *= ex2_mufu(end - cs[i]); });
         {
