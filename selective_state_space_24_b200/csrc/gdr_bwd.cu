@@ -67,12 +67,58 @@ struct Layout {
     __host__ __device__ size_t dS() const { return S0() + (size_t)V * K; }
 };
 
-// Pitches of shared tiles (in elements): a fragment's lanes read four
-// neighbouring k of eight rows, or eight neighbours of four rows; with these
-// either way is free of bank conflicts, or nearly.
-constexpr int pf(int n) { return n + 20; }   // float32
-constexpr int ph(int n) { return n + 8; }    // bf16
-constexpr int kPX = kC + 4;
+// Pitches of shared tiles (in elements).  A fragment's lanes read pairs of
+// neighbouring k, either along eight rows (64 or, for bf16, 32 bits a lane) or
+// down eight columns: free of bank conflicts for the way named.
+constexpr int pr(int n) { return n + 8; }   // float32, k along the row
+constexpr int pc(int n) { return n + 4; }   // float32, k down the column
+constexpr int ph(int n) { return n + 8; }   // bf16
+constexpr int kPX = pc(kC), kPN = pc(kSlice);
+
+// An operand: the values of k and k + 1 (k even) for index i of its other dimension.
+struct RowF {   // float32, k along the row
+    const float *p;
+    int pitch;
+    __device__ __forceinline__ float2 operator()(int i, int k) const
+    {
+        return *reinterpret_cast<const float2 *>(p + i * pitch + k);
+    }
+};
+struct ColF {   // float32, k down the column
+    const float *p;
+    int pitch;
+    __device__ __forceinline__ float2 operator()(int i, int k) const
+    {
+        return make_float2(p[k * pitch + i], p[(k + 1) * pitch + i]);
+    }
+};
+struct RowH {   // the same for bf16
+    const __nv_bfloat16 *p;
+    int pitch;
+    __device__ __forceinline__ float2 operator()(int i, int k) const
+    {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(p + i * pitch + k);
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+};
+struct ColH {
+    const __nv_bfloat16 *p;
+    int pitch;
+    __device__ __forceinline__ float2 operator()(int i, int k) const
+    {
+        return make_float2(__bfloat162float(p[k * pitch + i]), __bfloat162float(p[(k + 1) * pitch + i]));
+    }
+};
+template <class F> struct Scaled {   // times a factor of k
+    F f;
+    const float *v;
+    __device__ __forceinline__ float2 operator()(int i, int k) const
+    {
+        const float2 x = f(i, k), y = *reinterpret_cast<const float2 *>(v + k);
+        return make_float2(x.x * y.x, x.y * y.y);
+    }
+};
+template <class F> __device__ __forceinline__ Scaled<F> scaled(F f, const float *v) { return Scaled<F>{f, v}; }
 
 __device__ __forceinline__ float bf(const bf16 *p) { return __bfloat162float(*p); }
 
@@ -101,8 +147,10 @@ template <Part P, int N> __device__ __forceinline__ void parts(const float (&x)[
     }
 }
 
-// A warp's tile: acc += a(m0 + .., k) b(k, n0 + ..), MT x 16 rows, NT x 8
-// columns.  Element e of acc[m][n] is row m0 + 16 m + lane / 4 + 8 (e / 2),
+// A warp's tile: acc += sum over k of a(m0 + .., k) b(n0 + .., k), MT x 16
+// rows, NT x 8 columns.  (The tensor core's slots t and t + 4 of k take k
+// = 2 t and 2 t + 1 of both operands: the order within a sum is free, and so a
+// lane's two values are neighbours.)  Element e of acc[m][n] is row m0 + 16 m + lane / 4 + 8 (e / 2),
 // column n0 + 8 n + 2 (lane mod 4) + e mod 2.  The products of one part go
 // over the whole tile before those of the next, so that an accumulator is not
 // waited for; tiles of few accumulators keep one set for each part.
@@ -128,13 +176,14 @@ __device__ __forceinline__ void mm(float (&acc)[MT][NT][4], int m0, int n0, int 
 #pragma unroll
         for (int m = 0; m < MT; m++) {
             const int r = m0 + 16 * m + g;
-            const float x[4] = {a(r, k + t), a(r + 8, k + t), a(r, k + t + 4), a(r + 8, k + t + 4)};
+            const float2 u = a(r, k + 2 * t), v = a(r + 8, k + 2 * t);
+            const float x[4] = {u.x, v.x, u.y, v.y};
             parts<PA>(x, ah[m], al[m]);
         }
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            const int c = n0 + 8 * n + g;
-            const float y[2] = {b(k + t, c), b(k + t + 4, c)};
+            const float2 u = b(n0 + 8 * n + g, k + 2 * t);
+            const float y[2] = {u.x, u.y};
             parts<PB>(y, bh[n], bl[n]);
         }
         if (PB == kTwo)
@@ -274,7 +323,7 @@ __device__ __forceinline__ void load_slice(float *dst, const float *src, int ld)
 {
     for (int x = threadIdx.x; x < kC * kSlice / 4; x += kThreads) {
         const int r = x / (kSlice / 4), c = (x % (kSlice / 4)) * 4;
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * (kSlice + 8) + c);
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * kPN + c);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + (size_t)r * ld + c) : "memory");
     }
 }
@@ -312,7 +361,7 @@ __device__ __forceinline__ Where where(const GdrArgs &a, int64_t bh, int n)
 template <int K, int V> struct PrepSmem {
     bf16 k[kC * ph(K)], q[kC * ph(K)], v[kC * ph(V)], o[kC * ph(V)];
     float a[kC * kPX], t[kC * kPX], p[kC * kPX];
-    float cs[kC], b[kC], rk[kC], rq[kC];
+    float cs[kC], b[kC], rk[kC], rq[kC], wf[kC];   // wf: b c / |k|
 };
 template <int K, int V>
 __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, const Layout lay)
@@ -364,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
         qq = warp_sum(qq);
         if (lane == 0) {
             s.rk[r] = a.l2norm ? rsqrtf(kk + kL2Eps) : 1.f;
+            s.wf[r] = s.b[r] * ex2_mufu(s.cs[r]) * s.rk[r];
             s.rq[r] = a.scale * (a.l2norm ? rsqrtf(qq + kL2Eps) : 1.f);
         }
     }
@@ -407,13 +457,16 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
             s.t[i * kPX + c0 + j] = x[j];
     }
     __syncthreads();
-    auto A = [&](int r0, int c0) { return [&s, r0, c0](int i, int k) { return s.a[(r0 + i) * kPX + c0 + k]; }; };
-    auto T = [&](int r0, int c0) { return [&s, r0, c0](int i, int k) { return s.t[(r0 + i) * kPX + c0 + k]; }; };
+    // blocks as left operands (k along the row) and right ones (k down the column)
+    auto Tl = [&](int r0, int c0) { return RowF{s.t + r0 * kPX + c0, kPX}; };
+    auto Al = [&](int r0, int c0) { return RowF{s.a + r0 * kPX + c0, kPX}; };
+    auto Tr = [&](int r0, int c0) { return ColF{s.t + r0 * kPX + c0, kPX}; };
+    auto Ar = [&](int r0, int c0) { return ColF{s.a + r0 * kPX + c0, kPX}; };
     if (warp < 4) {   // A21 T11 of both pairs of 16 blocks, in the place of A21
         const int r0 = 32 * (warp >> 1) + 16, c0 = r0 - 16, n0 = 8 * (warp & 1);
         float x[1][1][4];
         zero(x);
-        mm<kTwo, kTwo>(x, 0, n0, 16, A(r0, c0), T(c0, c0));
+        mm<kTwo, kTwo>(x, 0, n0, 16, Al(r0, c0), Tr(c0, c0));
         __syncwarp();
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");   // both warps have read A21
         each(x, 0, n0, [&](int i, int j, float v) { s.a[(r0 + i) * kPX + c0 + j] = v; });
@@ -423,19 +476,19 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
         const int r0 = 32 * (warp >> 1) + 16, c0 = r0 - 16, n0 = 8 * (warp & 1);
         float x[1][1][4];
         zero(x);
-        mm<kTwo, kTwo>(x, 0, n0, 16, T(r0, r0), A(r0, c0));
+        mm<kTwo, kTwo>(x, 0, n0, 16, Tl(r0, r0), Ar(r0, c0));
         each(x, 0, n0, [&](int i, int j, float v) { s.t[(r0 + i) * kPX + c0 + j] = -v; });
     }
     __syncthreads();
     {   // 32 x 32: warps 2 (rows) x 4 (columns of 8)
         float x[1][1][4];
         zero(x);
-        mm<kTwo, kTwo>(x, m0 / 2, 8 * wn, 32, A(32, 0), T(0, 0));
+        mm<kTwo, kTwo>(x, m0 / 2, 8 * wn, 32, Al(32, 0), Tr(0, 0));
         __syncthreads();
         each(x, m0 / 2, 8 * wn, [&](int i, int j, float v) { s.a[(32 + i) * kPX + j] = v; });
         __syncthreads();
         zero(x);
-        mm<kTwo, kTwo>(x, m0 / 2, 8 * wn, 32, T(32, 32), A(32, 0));
+        mm<kTwo, kTwo>(x, m0 / 2, 8 * wn, 32, Tl(32, 32), Ar(32, 0));
         each(x, m0 / 2, 8 * wn, [&](int i, int j, float v) { s.t[(32 + i) * kPX + j] = -v; });
     }
     __syncthreads();
@@ -451,34 +504,29 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
     {
         float acc[2][K / 32][4];
         zero(acc);
-        mm<kTwo, kExact>(acc, m0, K / 4 * wn, kC,
-                         [&](int i, int k) { return s.t[i * kPX + k] * (s.b[k] * ex2_mufu(s.cs[k]) * s.rk[k]); },
-                         [&](int k, int j) { return bf(&s.k[k * ph(K) + j]); });
+        mm<kTwo, kExact>(acc, m0, K / 4 * wn, kC, scaled(RowF{s.t, kPX}, s.wf), ColH{s.k, ph(K)});
         pairs(acc, m0, K / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.W() + i * K + j, x, y); });
     }
     float acc[2][V / 32][4];
     zero(acc);
-    mm<kTwo, kExact>(acc, m0, V / 4 * wn, kC, [&](int i, int k) { return s.t[i * kPX + k] * s.b[k]; },
-                     [&](int k, int j) { return bf(&s.v[k * ph(V) + j]); });
+    mm<kTwo, kExact>(acc, m0, V / 4 * wn, kC, scaled(RowF{s.t, kPX}, s.b), ColH{s.v, ph(V)});
     pairs(acc, m0, V / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.U() + i * V + j, x, y); });
     zero(acc);
-    mm<kTwo, kExact>(acc, m0, V / 4 * wn, kC, [&](int i, int k) { return s.p[k * kPX + i]; },
-                     [&](int k, int j) { return bf(&s.o[k * ph(V) + j]); });
+    mm<kTwo, kExact>(acc, m0, V / 4 * wn, kC, ColF{s.p, kPX}, ColH{s.o, ph(V)});
     pairs(acc, m0, V / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.dN() + i * V + j, x, y); });
 }
 
 // ---- 2. forward over the chunks, 32 state rows per block: S0, and N in U's place
 template <int K> struct ChainSmem {
-    float w[2][kC * pf(K)];
+    float w[2][kC * pr(K)];
     bf16 k[2][kC * ph(K)];
-    float u[2][kC * (kSlice + 8)], v[2][4 * kC];   // U; cs, b, 1 / |k|, scale / |q|
-    float s[kSlice * pf(K)], n[kC * (kSlice + 8)];
+    float u[2][kC * kPN], v[2][4 * kC];   // U; cs, b, 1 / |k|, scale / |q|
+    float s[kSlice * pr(K)], n[kC * kPN];
 };
 template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const GdrArgs a, const Layout lay)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     ChainSmem<K> &s = *reinterpret_cast<ChainSmem<K> *>(raw);
-    constexpr int pn = kSlice + 8;
     const int slices = a.V / kSlice, warp = threadIdx.x >> 5;
     const int64_t bh = blockIdx.x / slices;
     const int v0 = (blockIdx.x % slices) * kSlice;
@@ -486,7 +534,7 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
     auto fetch = [&](int n) {
         if (n < lay.NC) {
             const Where w = where(a, bh, n);
-            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pf(K));
+            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pr(K));
             load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
             load_slice(s.u[n & 1], base + lay.base(bh, n) + lay.U() + v0, a.V);
             load_scalars(s.v[n & 1], base + lay.base(bh, n));
@@ -495,7 +543,7 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
     };
     fetch(0);
     for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-        s.s[(x / K) * pf(K) + x % K] = a.init ? a.init[((size_t)bh * a.V + v0) * K + x] : 0.f;
+        s.s[(x / K) * pr(K) + x % K] = a.init ? a.init[((size_t)bh * a.V + v0) * K + x] : 0.f;
     const int mN = 16 * (warp >> 1), nN = 16 * (warp & 1);   // N: 64 x 32 as 4 x 2 warps
     constexpr int NT = K / 64;                               // the state: 32 x K as 1 x 8
     for (int n = 0; n < lay.NC; n++) {
@@ -507,32 +555,30 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
         const float end = cs[kC - 1];
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.S0() + (size_t)v0 * K + x) =
-                *reinterpret_cast<const float4 *>(&s.s[(x / K) * pf(K) + x % K]);
+                *reinterpret_cast<const float4 *>(&s.s[(x / K) * pr(K) + x % K]);
         const float *W = s.w[n & 1];
         const bf16 *Kt = s.k[n & 1];
         float acc[1][2][4];
         zero(acc);
-        mm<kTwo, kTwo>(acc, mN, nN, K, [&](int i, int k) { return W[i * pf(K) + k]; },
-                       [&](int k, int j) { return s.s[j * pf(K) + k]; });
+        mm<kTwo, kTwo>(acc, mN, nN, K, RowF{W, pr(K)}, RowF{s.s, pr(K)});
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
             const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
-                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * pn + j]);
+                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * kPN + j]);
                 x = f2.x - x, y = f2.y - y;
                 st2(ws + lay.U() + i * a.V + v0 + j, x, y);
                 const float f = e[(i - i0) >> 3];
-                st2(&s.n[i * pn + j], x * f, y * f);
+                st2(&s.n[i * kPN + j], x * f, y * f);
             });
         }
         __syncthreads();
         float up[2][NT][4];
         zero(up);
-        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, [&](int i, int k) { return s.n[k * pn + i]; },
-                         [&](int k, int j) { return bf(&Kt[k * ph(K) + j]); });
+        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, ColF{s.n, kPN}, ColH{Kt, ph(K)});
         const float dec = ex2_mufu(end);
         each(up, 0, 8 * NT * warp, [&](int i, int j, float v) {
-            float *p = &s.s[i * pf(K) + j];
+            float *p = &s.s[i * pr(K) + j];
             *p = fmaf(dec, *p, v);
         });
         __syncthreads();
@@ -541,10 +587,10 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(con
 
 // ---- 3. in reverse: dS1, and dN in the place of P^T dO
 template <int K> struct ReverseSmem {
-    float w[2][kC * pf(K)];
+    float w[2][kC * pc(K)];
     bf16 k[2][kC * ph(K)], q[2][kC * ph(K)], o[2][kC * ph(kSlice)];
-    float u[2][kC * (kSlice + 8)], v[2][4 * kC];   // P^T dO; scalars
-    float g[kSlice * pf(K)], n[kC * (kSlice + 8)];
+    float u[2][kC * kPN], v[2][4 * kC];   // P^T dO; scalars
+    float g[kSlice * pr(K)], n[kC * kPN];
     float f[kC];
 };
 template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(const GdrBwdArgs ga, const Layout lay)
@@ -552,7 +598,6 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
     extern __shared__ __align__(16) uint8_t raw[];
     ReverseSmem<K> &s = *reinterpret_cast<ReverseSmem<K> *>(raw);
     const GdrArgs &a = ga.f;
-    constexpr int pn = kSlice + 8;
     const int slices = a.V / kSlice, warp = threadIdx.x >> 5;
     const int64_t bh = blockIdx.x / slices;
     const int v0 = (blockIdx.x % slices) * kSlice;
@@ -560,7 +605,7 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
     auto fetch = [&](int n) {
         if (n >= 0) {
             const Where w = where(a, bh, n);
-            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pf(K));
+            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pc(K));
             load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
             load_rows<K>(s.q[n & 1], static_cast<const bf16 *>(a.q) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
             load_rows<kSlice>(s.o[n & 1], static_cast<const bf16 *>(ga.dout) + (w.tok * a.Hv + w.h) * a.V + v0,
@@ -572,7 +617,7 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
     };
     fetch(lay.NC - 1);
     for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-        s.g[(x / K) * pf(K) + x % K] = ga.dlast ? ga.dlast[((size_t)bh * a.V + v0) * K + x] : 0.f;
+        s.g[(x / K) * pr(K) + x % K] = ga.dlast ? ga.dlast[((size_t)bh * a.V + v0) * K + x] : 0.f;
     const int mN = 16 * (warp >> 1), nN = 16 * (warp & 1);
     constexpr int NT = K / 64;
     for (int n = lay.NC - 1; n >= 0; n--) {
@@ -586,49 +631,46 @@ template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(c
             s.f[threadIdx.x] = rq[threadIdx.x] * ex2_mufu(cs[threadIdx.x]);
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.dS() + (size_t)v0 * K + x) =
-                *reinterpret_cast<const float4 *>(&s.g[(x / K) * pf(K) + x % K]);
+                *reinterpret_cast<const float4 *>(&s.g[(x / K) * pr(K) + x % K]);
         const float *W = s.w[n & 1];
         const bf16 *Kt = s.k[n & 1], *Qt = s.q[n & 1], *Ot = s.o[n & 1];
         float acc[1][2][4];
         zero(acc);
-        mm<kExact, kTwo>(acc, mN, nN, K, [&](int i, int k) { return bf(&Kt[i * ph(K) + k]); },
-                         [&](int k, int j) { return s.g[j * pf(K) + k]; });
+        mm<kExact, kTwo>(acc, mN, nN, K, RowH{Kt, ph(K)}, RowF{s.g, pr(K)});
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
             const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
-                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * pn + j]);
+                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * kPN + j]);
                 const float f = e[(i - i0) >> 3];
                 x = fmaf(f, x, f2.x), y = fmaf(f, y, f2.y);
                 st2(ws + lay.dN() + i * a.V + v0 + j, x, y);
-                st2(&s.n[i * pn + j], -x, -y);
+                st2(&s.n[i * kPN + j], -x, -y);
             });
         }
         __syncthreads();
         float up[2][NT][4];
         zero(up);
-        mm<kTwo, kTwo>(up, 0, 8 * NT * warp, kC, [&](int i, int k) { return s.n[k * pn + i]; },
-                       [&](int k, int j) { return W[k * pf(K) + j]; });
-        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, [&](int i, int k) { return s.f[k] * bf(&Ot[k * ph(kSlice) + i]); },
-                         [&](int k, int j) { return bf(&Qt[k * ph(K) + j]); });
+        mm<kTwo, kTwo>(up, 0, 8 * NT * warp, kC, ColF{s.n, kPN}, ColF{W, pc(K)});
+        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, scaled(ColH{Ot, ph(kSlice)}, s.f), ColH{Qt, ph(K)});
         const float dec = ex2_mufu(end);
         each(up, 0, 8 * NT * warp, [&](int i, int j, float v) {
-            float *p = &s.g[i * pf(K) + j];
+            float *p = &s.g[i * pr(K) + j];
             *p = fmaf(dec, *p, v);
         });
         __syncthreads();
     }
     if (ga.dinit)
         for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
-            ga.dinit[((size_t)bh * a.V + v0) * K + x] = s.g[(x / K) * pf(K) + x % K];
+            ga.dinit[((size_t)bh * a.V + v0) * K + x] = s.g[(x / K) * pr(K) + x % K];
 }
 
 // ---- 4. per chunk and key head: every gradient
 template <int K, int V> struct GradSmem {
     bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(V)];
-    float n[kC * pf(V)], r[kC * pf(V)], x[kC * kPX];
-    float t[kC * kPX], m[2][kSlice * pf(K)];   // T; 32 rows of a state, the next 32
-    float cs[4 * kC];       // cs, b, rk, rq as in the workspace
+    float n[kC * pr(V)], r[kC * pr(V)], x[kC * kPX];
+    float t[kC * kPX], m[2][kSlice * pc(K)];   // T; 32 rows of a state, the next 32
+    float cs[4 * kC], brk[kC];   // cs, b, rk, rq as in the workspace; b rk
     float dcs[kC], sum[6][4][kC], red[8];   // sum: row sums of each column of warps
 };
 template <int K, int V>
@@ -680,28 +722,29 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         __syncthreads();
         s.cs[threadIdx.x] = ws[threadIdx.x];
         load_rows<V>(s.o, static_cast<const bf16 *>(ga.dout) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid);
-        load_f<kC, V>(s.n, ws + lay.U(), pf(V));
-        load_f<kC, V>(s.r, ws + lay.dN(), pf(V));
+        load_f<kC, V>(s.n, ws + lay.U(), pr(V));
+        load_f<kC, V>(s.r, ws + lay.dN(), pr(V));
         load_f<kC, kC>(s.t, ws + lay.T(), kPX);
         cp_commit();
         // S0 and then dS1, 32 rows at a time, two pieces on their way
         constexpr int kPieces = V / kSlice;
         auto fetch = [&](int i) {
             if (i < 2 * kPieces)
-                load_f<kSlice, K>(s.m[i & 1], (i < kPieces ? S0 : dS - (size_t)V * K) + (size_t)i * kSlice * K, pf(K));
+                load_f<kSlice, K>(s.m[i & 1], (i < kPieces ? S0 : dS - (size_t)V * K) + (size_t)i * kSlice * K, pc(K));
             cp_commit();
         };
         fetch(0);
         fetch(1);
         cp_wait<2>();
         __syncthreads();
+        if (threadIdx.x < kC)   // read much later
+            s.brk[threadIdx.x] = bb[threadIdx.x] * rk[threadIdx.x];
         const float end = cs[kC - 1];
         // R' = T^T dN
         {
             float r[2][NV][4];
             zero(r);
-            mm<kTwo, kTwo>(r, m0, nV, kC, [&](int i, int k) { return s.t[k * kPX + i]; },
-                           [&](int k, int j) { return s.r[k * pf(V) + j]; });
+            mm<kTwo, kTwo>(r, m0, nV, kC, ColF{s.t, kPX}, ColF{s.r, pr(V)});
             __syncthreads();
             float dbr[4] = {};
 #pragma unroll
@@ -712,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
                     for (int e = 0; e < 2; e++) {
                         const int i = m0 + 16 * m + gq + 8 * e, j = nV + 8 * q + 2 * tq;
                         const float x = r[m][q][2 * e], y = r[m][q][2 * e + 1];
-                        st2(&s.r[i * pf(V) + j], x, y);
+                        st2(&s.r[i * pr(V) + j], x, y);
                         if (i < valid) {
                             const __nv_bfloat162 vv = *reinterpret_cast<const __nv_bfloat162 *>(vp + (size_t)i * a.Hv * V + j);
                             dbr[2 * m + e] = fmaf(x, __low2float(vv), fmaf(y, __high2float(vv), dbr[2 * m + e]));
@@ -728,9 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         {
             zero(xa);
             zero(xp);
-            auto Nt = [&](int k, int j) { return s.n[j * pf(V) + k]; };
-            mm<kTwo, kTwo>(xa, m0, nC, V, [&](int i, int k) { return s.r[i * pf(V) + k]; }, Nt);
-            mm<kExact, kTwo>(xp, m0, nC, V, [&](int i, int k) { return bf(&s.o[i * ph(V) + k]); }, Nt);
+            mm<kTwo, kTwo>(xa, m0, nC, V, RowF{s.r, pr(V)}, RowF{s.n, pr(V)});
+            mm<kExact, kTwo>(xp, m0, nC, V, RowH{s.o, ph(V)}, RowF{s.n, pr(V)});
             each(xa, m0, nC, [&](int i, int j, float &v) { v = j < i ? -v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
             each(xp, m0, nC, [&](int i, int j, float &v) { v = j <= i ? v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
             float kk[2][2][4], qk[2][2][4];
@@ -790,9 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             const float *St = s.m[i & 1];
             cp_wait<1>();
             __syncthreads();
-            auto Sf = [&](int k, int j) { return St[k * pf(K) + j]; };
-            mm<kTwo, kTwo>(Y, m0, nK, kSlice, [&](int r, int k) { return s.r[r * pf(V) + v0 + k]; }, Sf);
-            mm<kExact, kTwo>(q, m0, nK, kSlice, [&](int r, int k) { return bf(&s.o[r * ph(V) + v0 + k]); }, Sf);
+            mm<kTwo, kTwo>(Y, m0, nK, kSlice, RowF{s.r + v0, pr(V)}, ColF{St, pc(K)});
+            mm<kExact, kTwo>(q, m0, nK, kSlice, RowH{s.o + v0, ph(V)}, ColF{St, pc(K)});
             __syncthreads();
             fetch(i + 2);
         }
@@ -810,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             put_rows(1, qq);   // s
         }
         // the rest of Y, and of q: one part is enough for their bf16 results
-        mm<kOne, kExact>(Y, m0, nK, kC, [&](int i, int k) { return s.x[i * kPX + k] * rk[k]; }, Kt);
+        mm<kOne, kExact>(Y, m0, nK, kC, scaled(RowF{s.x, kPX}, rk), ColH{s.k, ph(K)});
         {
             float ky[4] = {};
             dots(Y, m0, nK, Kt, ky);
@@ -836,11 +877,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             const float *St = s.m[i & 1];
             cp_wait<1>();
             __syncthreads();
-            mm<kTwo, kTwo>(Y, m0, nK, kSlice, [&](int r, int k) { return s.n[r * pf(V) + v0 + k]; },
-                           [&](int k, int j) { return St[k * pf(K) + j]; });
+            mm<kTwo, kTwo>(Y, m0, nK, kSlice, RowF{s.n + v0, pr(V)}, ColF{St, pc(K)});
             for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4) {   // c_end <dS1, S0>
                 const float4 f = *reinterpret_cast<const float4 *>(S0 + (size_t)v0 * K + x);
-                const float4 d = *reinterpret_cast<const float4 *>(&St[(x / K) * pf(K) + x % K]);
+                const float4 d = *reinterpret_cast<const float4 *>(&St[(x / K) * pc(K) + x % K]);
                 through = fmaf(dec * d.x, f.x, fmaf(dec * d.y, f.y, fmaf(dec * d.z, f.z, fmaf(dec * d.w, f.w, through))));
             }
             __syncthreads();
@@ -855,15 +895,15 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
                 kz[x] *= rk[row_of(x)];
             put_rows(3, kz);   // z
         }
-        mm<kOne, kExact>(Y, m0, nK, kC, [&](int i, int k) { return s.x[k * kPX + i] * (bb[k] * rk[k]); }, Kt);
+        mm<kOne, kExact>(Y, m0, nK, kC, scaled(ColF{s.x, kPX}, s.brk), ColH{s.k, ph(K)});
         __syncthreads();
         each(xp, m0, nC, [&](int i, int j, float v) { s.x[i * kPX + j] = v; });
         through = warp_sum(through);
         if (lane == 0)
             s.red[warp] = through;
         __syncthreads();
-        mm<kOne, kExact>(Y, m0, nK, kC, [&](int i, int k) { return s.x[k * kPX + i] * rq[k]; }, Qt);
-        mm<kOne, kExact>(q, m0, nK, kC, [&](int i, int k) { return s.x[i * kPX + k] * rk[k]; }, Kt);
+        mm<kOne, kExact>(Y, m0, nK, kC, scaled(ColF{s.x, kPX}, rq), ColH{s.q, ph(K)});
+        mm<kOne, kExact>(q, m0, nK, kC, scaled(RowF{s.x, kPX}, rk), ColH{s.k, ph(K)});
 #pragma unroll
         for (int m = 0; m < 2; m++)
 #pragma unroll
