@@ -359,12 +359,16 @@ __device__ __forceinline__ Where where(const GdrArgs &a, int64_t bh, int n)
 
 // ---- 1. per chunk and value head: the scalars, T, W, U = T diag(b) V and P^T dO
 template <int K, int V> struct PrepSmem {
-    bf16 k[kC * ph(K)], q[kC * ph(K)], v[kC * ph(V)], o[kC * ph(V)];
-    float a[kC * kPX], t[kC * kPX], p[kC * kPX];
+    bf16 k[kC * ph(K)], v[kC * ph(V)], o[kC * ph(V)];
+    union {   // P takes Q's place: two blocks fit on an SM
+        bf16 q[kC * ph(K)];
+        float p[kC * kPX];
+    };
+    float a[kC * kPX], t[kC * kPX];
     float cs[kC], b[kC], rk[kC], rq[kC], wf[kC];   // wf: b c / |k|
 };
 template <int K, int V>
-__global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, const Layout lay)
+__global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, const Layout lay)
 {
     extern __shared__ __align__(16) uint8_t raw[];
     PrepSmem<K, V> &s = *reinterpret_cast<PrepSmem<K, V> *>(raw);
@@ -425,6 +429,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const GdrBwdArgs g, cons
         zero(qk);
         mm16(kk, m0, 16 * wn, K, s.k, ph(K), s.k, ph(K));
         mm16(qk, m0, 16 * wn, K, s.q, ph(K), s.k, ph(K));
+        __syncthreads();   // Q is done with
         each(kk, m0, 16 * wn, [&](int i, int j, float v) {
             s.a[i * kPX + j] = j < i ? s.b[i] * ex2_mufu(s.cs[i] - s.cs[j]) * s.rk[i] * s.rk[j] * v : 0.f;
             s.t[i * kPX + j] = 0.f;
