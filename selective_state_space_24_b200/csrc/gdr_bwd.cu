@@ -521,153 +521,182 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
     pairs(acc, m0, V / 4 * wn, [&](int i, int j, float x, float y) { st2(ws + lay.dN() + i * V + j, x, y); });
 }
 
-// ---- 2. forward over the chunks, 32 state rows per block: S0, and N in U's place
+// ---- 2. forward over the chunks (S0, and N in U's place) and 3. in reverse (dS1,
+// and dN in the place of P^T dO): neither needs the other, so one launch takes
+// both, 32 state rows per block, one block of each kind to an SM.  Tiles have
+// one buffer each; a phase's next tiles are fetched while the other phase runs.
 template <int K> struct ChainSmem {
-    float w[2][kC * pr(K)];
-    bf16 k[2][kC * ph(K)];
-    float u[2][kC * kPN], v[2][4 * kC];   // U; cs, b, 1 / |k|, scale / |q|
+    float w[kC * pr(K)];
+    bf16 k[kC * ph(K)];
+    float u[kC * kPN], v[4 * kC];   // U; cs, b, 1 / |k|, scale / |q|
     float s[kSlice * pr(K)], n[kC * kPN];
 };
-template <int K> __global__ void __launch_bounds__(kThreads, 1) chain_kernel(const GdrArgs a, const Layout lay)
+template <int K> __device__ __forceinline__ void forward_chain(const GdrArgs &a, const Layout &lay, ChainSmem<K> &s, int64_t bh, int v0)
 {
-    extern __shared__ __align__(16) uint8_t raw[];
-    ChainSmem<K> &s = *reinterpret_cast<ChainSmem<K> *>(raw);
-    const int slices = a.V / kSlice, warp = threadIdx.x >> 5;
-    const int64_t bh = blockIdx.x / slices;
-    const int v0 = (blockIdx.x % slices) * kSlice;
+    const int warp = threadIdx.x >> 5;
     float *base = static_cast<float *>(a.workspace);
-    auto fetch = [&](int n) {
+    auto fetch1 = [&](int n) {   // for S W^T
         if (n < lay.NC) {
-            const Where w = where(a, bh, n);
-            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pr(K));
-            load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
-            load_slice(s.u[n & 1], base + lay.base(bh, n) + lay.U() + v0, a.V);
-            load_scalars(s.v[n & 1], base + lay.base(bh, n));
+            const float *ws = base + lay.base(bh, n);
+            load_f<kC, K>(s.w, ws + lay.W(), pr(K));
+            load_slice(s.u, ws + lay.U() + v0, a.V);
+            load_scalars(s.v, ws);
         }
         cp_commit();
     };
-    fetch(0);
+    auto fetch2 = [&](int n) {   // for N^T K
+        if (n < lay.NC) {
+            const Where w = where(a, bh, n);
+            load_rows<K>(s.k, static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+        }
+        cp_commit();
+    };
+    fetch1(0);
+    fetch2(0);
     for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
         s.s[(x / K) * pr(K) + x % K] = a.init ? a.init[((size_t)bh * a.V + v0) * K + x] : 0.f;
     const int mN = 16 * (warp >> 1), nN = 16 * (warp & 1);   // N: 64 x 32 as 4 x 2 warps
     constexpr int NT = K / 64;                               // the state: 32 x K as 1 x 8
     for (int n = 0; n < lay.NC; n++) {
         float *ws = base + lay.base(bh, n);
-        fetch(n + 1);
         cp_wait<1>();
         __syncthreads();
-        const float *u = s.u[n & 1], *cs = s.v[n & 1], *rk = cs + 2 * kC;
-        const float end = cs[kC - 1];
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.S0() + (size_t)v0 * K + x) =
                 *reinterpret_cast<const float4 *>(&s.s[(x / K) * pr(K) + x % K]);
-        const float *W = s.w[n & 1];
-        const bf16 *Kt = s.k[n & 1];
+        const float *cs = s.v, *rk = s.v + 2 * kC;
+        const float end = cs[kC - 1], dec = ex2_mufu(end);
         float acc[1][2][4];
         zero(acc);
-        mm<kTwo, kTwo>(acc, mN, nN, K, RowF{W, pr(K)}, RowF{s.s, pr(K)});
+        mm<kTwo, kTwo>(acc, mN, nN, K, RowF{s.w, pr(K)}, RowF{s.s, pr(K)});
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
             const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
-                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * kPN + j]);
-                x = f2.x - x, y = f2.y - y;
+                const float2 u = *reinterpret_cast<const float2 *>(&s.u[i * kPN + j]);
+                x = u.x - x, y = u.y - y;
                 st2(ws + lay.U() + i * a.V + v0 + j, x, y);
                 const float f = e[(i - i0) >> 3];
                 st2(&s.n[i * kPN + j], x * f, y * f);
             });
         }
         __syncthreads();
+        fetch1(n + 1);
+        cp_wait<1>();
+        __syncthreads();
         float up[2][NT][4];
         zero(up);
-        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, ColF{s.n, kPN}, ColH{Kt, ph(K)});
-        const float dec = ex2_mufu(end);
+        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, ColF{s.n, kPN}, ColH{s.k, ph(K)});
         each(up, 0, 8 * NT * warp, [&](int i, int j, float v) {
             float *p = &s.s[i * pr(K) + j];
             *p = fmaf(dec, *p, v);
         });
         __syncthreads();
+        fetch2(n + 1);
     }
 }
 
-// ---- 3. in reverse: dS1, and dN in the place of P^T dO
 template <int K> struct ReverseSmem {
-    float w[2][kC * pc(K)];
-    bf16 k[2][kC * ph(K)], q[2][kC * ph(K)], o[2][kC * ph(kSlice)];
-    float u[2][kC * kPN], v[2][4 * kC];   // P^T dO; scalars
+    float w[kC * pc(K)];
+    bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(kSlice)];
+    float u[kC * kPN], v[4 * kC];   // P^T dO; scalars
     float g[kSlice * pr(K)], n[kC * kPN];
     float f[kC];
 };
-template <int K> __global__ void __launch_bounds__(kThreads, 1) reverse_kernel(const GdrBwdArgs ga, const Layout lay)
+template <int K> __device__ __forceinline__ void reverse_chain(const GdrBwdArgs &ga, const Layout &lay, ReverseSmem<K> &s, int64_t bh, int v0)
 {
-    extern __shared__ __align__(16) uint8_t raw[];
-    ReverseSmem<K> &s = *reinterpret_cast<ReverseSmem<K> *>(raw);
     const GdrArgs &a = ga.f;
-    const int slices = a.V / kSlice, warp = threadIdx.x >> 5;
-    const int64_t bh = blockIdx.x / slices;
-    const int v0 = (blockIdx.x % slices) * kSlice;
+    const int warp = threadIdx.x >> 5;
     float *base = static_cast<float *>(a.workspace);
-    auto fetch = [&](int n) {
+    auto fetch1 = [&](int n) {   // for K dS^T
         if (n >= 0) {
             const Where w = where(a, bh, n);
-            load_f<kC, K>(s.w[n & 1], base + lay.base(bh, n) + lay.W(), pc(K));
-            load_rows<K>(s.k[n & 1], static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
-            load_rows<K>(s.q[n & 1], static_cast<const bf16 *>(a.q) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
-            load_rows<kSlice>(s.o[n & 1], static_cast<const bf16 *>(ga.dout) + (w.tok * a.Hv + w.h) * a.V + v0,
-                              (size_t)a.Hv * a.V, w.valid);
-            load_slice(s.u[n & 1], base + lay.base(bh, n) + lay.dN() + v0, a.V);
-            load_scalars(s.v[n & 1], base + lay.base(bh, n));
+            const float *ws = base + lay.base(bh, n);
+            load_rows<K>(s.k, static_cast<const bf16 *>(a.k) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+            load_slice(s.u, ws + lay.dN() + v0, a.V);
+            load_scalars(s.v, ws);
         }
         cp_commit();
     };
-    fetch(lay.NC - 1);
+    auto fetch2 = [&](int n) {   // for dN^T W and dO^T Q
+        if (n >= 0) {
+            const Where w = where(a, bh, n);
+            load_f<kC, K>(s.w, base + lay.base(bh, n) + lay.W(), pc(K));
+            load_rows<K>(s.q, static_cast<const bf16 *>(a.q) + (w.tok * a.Hk + w.hk) * K, (size_t)a.Hk * K, w.valid);
+            load_rows<kSlice>(s.o, static_cast<const bf16 *>(ga.dout) + (w.tok * a.Hv + w.h) * a.V + v0, (size_t)a.Hv * a.V,
+                              w.valid);
+        }
+        cp_commit();
+    };
+    fetch1(lay.NC - 1);
+    fetch2(lay.NC - 1);
     for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
         s.g[(x / K) * pr(K) + x % K] = ga.dlast ? ga.dlast[((size_t)bh * a.V + v0) * K + x] : 0.f;
     const int mN = 16 * (warp >> 1), nN = 16 * (warp & 1);
     constexpr int NT = K / 64;
     for (int n = lay.NC - 1; n >= 0; n--) {
         float *ws = base + lay.base(bh, n);
-        fetch(n - 1);
         cp_wait<1>();
         __syncthreads();
-        const float *u = s.u[n & 1], *cs = s.v[n & 1], *rk = cs + 2 * kC, *rq = cs + 3 * kC;
-        const float end = cs[kC - 1];
+        const float *cs = s.v, *rk = s.v + 2 * kC, *rq = s.v + 3 * kC;
+        const float end = cs[kC - 1], dec = ex2_mufu(end);
         if (threadIdx.x < kC)
             s.f[threadIdx.x] = rq[threadIdx.x] * ex2_mufu(cs[threadIdx.x]);
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.dS() + (size_t)v0 * K + x) =
                 *reinterpret_cast<const float4 *>(&s.g[(x / K) * pr(K) + x % K]);
-        const float *W = s.w[n & 1];
-        const bf16 *Kt = s.k[n & 1], *Qt = s.q[n & 1], *Ot = s.o[n & 1];
         float acc[1][2][4];
         zero(acc);
-        mm<kExact, kTwo>(acc, mN, nN, K, RowH{Kt, ph(K)}, RowF{s.g, pr(K)});
+        mm<kExact, kTwo>(acc, mN, nN, K, RowH{s.k, ph(K)}, RowF{s.g, pr(K)});
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
             const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
-                const float2 f2 = *reinterpret_cast<const float2 *>(&u[i * kPN + j]);
+                const float2 u = *reinterpret_cast<const float2 *>(&s.u[i * kPN + j]);
                 const float f = e[(i - i0) >> 3];
-                x = fmaf(f, x, f2.x), y = fmaf(f, y, f2.y);
+                x = fmaf(f, x, u.x), y = fmaf(f, y, u.y);
                 st2(ws + lay.dN() + i * a.V + v0 + j, x, y);
                 st2(&s.n[i * kPN + j], -x, -y);
             });
         }
         __syncthreads();
+        fetch1(n - 1);
+        cp_wait<1>();
+        __syncthreads();
         float up[2][NT][4];
         zero(up);
-        mm<kTwo, kTwo>(up, 0, 8 * NT * warp, kC, ColF{s.n, kPN}, ColF{W, pc(K)});
-        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, scaled(ColH{Ot, ph(kSlice)}, s.f), ColH{Qt, ph(K)});
-        const float dec = ex2_mufu(end);
+        mm<kTwo, kTwo>(up, 0, 8 * NT * warp, kC, ColF{s.n, kPN}, ColF{s.w, pc(K)});
+        mm<kTwo, kExact>(up, 0, 8 * NT * warp, kC, scaled(ColH{s.o, ph(kSlice)}, s.f), ColH{s.q, ph(K)});
         each(up, 0, 8 * NT * warp, [&](int i, int j, float v) {
             float *p = &s.g[i * pr(K) + j];
             *p = fmaf(dec, *p, v);
         });
         __syncthreads();
+        fetch2(n - 1);
     }
     if (ga.dinit)
         for (int x = threadIdx.x; x < kSlice * K; x += kThreads)
             ga.dinit[((size_t)bh * a.V + v0) * K + x] = s.g[(x / K) * pr(K) + x % K];
+}
+
+template <int K> constexpr size_t chains_smem()
+{
+    return sizeof(ReverseSmem<K>) > sizeof(ChainSmem<K>) ? sizeof(ReverseSmem<K>) : sizeof(ChainSmem<K>);
+}
+template <int K> __global__ void __launch_bounds__(kThreads, 2) chains_kernel(const GdrBwdArgs g, const Layout lay, int chains)
+{
+    extern __shared__ __align__(16) uint8_t raw[];
+    const int slices = g.f.V / kSlice;
+    // blocks 0 .. chains - 1 run forward, the others in reverse: dealt out to
+    // the SMs in turn, both kinds are spread evenly
+    const bool reverse = (int)blockIdx.x >= chains;
+    const int at = reverse ? blockIdx.x - chains : blockIdx.x;
+    const int64_t bh = at / slices;
+    const int v0 = (at % slices) * kSlice;
+    if (reverse)
+        reverse_chain<K>(g, lay, *reinterpret_cast<ReverseSmem<K> *>(raw), bh, v0);
+    else
+        forward_chain<K>(g.f, lay, *reinterpret_cast<ChainSmem<K> *>(raw), bh, v0);
 }
 
 // ---- 4. per chunk and key head: every gradient
@@ -1026,7 +1055,7 @@ cudaError_t go(Kern kernel, int64_t blocks, size_t bytes, cudaStream_t st, Args.
 template <int K, int V> cudaError_t launch(const GdrBwdArgs &g, cudaStream_t st)
 {
     static_assert(sizeof(GradSmem<K, V>) <= 227 * 1024 && sizeof(PrepSmem<K, V>) <= 227 * 1024 &&
-                      sizeof(ReverseSmem<K>) <= 227 * 1024,
+                      2 * (chains_smem<K>() + 1024) <= 228 * 1024,
                   "shared memory of one block");
     const GdrArgs &a = g.f;
     const Layout l = layout(a);
@@ -1034,9 +1063,7 @@ template <int K, int V> cudaError_t launch(const GdrBwdArgs &g, cudaStream_t st)
     const int64_t chains = l.heads * (V / kSlice);
     cudaError_t e = go(prep_kernel<K, V>, l.heads * l.NC, sizeof(PrepSmem<K, V>), st, g, l);
     if (e == cudaSuccess)
-        e = go(chain_kernel<K>, chains, sizeof(ChainSmem<K>), st, a, l);
-    if (e == cudaSuccess)
-        e = go(reverse_kernel<K>, chains, sizeof(ReverseSmem<K>), st, g, l);
+        e = go(chains_kernel<K>, 2 * chains, chains_smem<K>(), st, g, l, (int)chains);
     if (e == cudaSuccess)
         e = go(grad_kernel<K, V>, (int64_t)a.Bsz * a.Hk * l.NC, sizeof(GradSmem<K, V>), st, g, l, partial);
     if (e != cudaSuccess)
