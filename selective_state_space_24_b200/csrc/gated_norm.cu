@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
             row_sum<1>(one, tpr, red, turn);
             sum[0] = one[0];
         }
-        const float r = rsqrtf(sum[0] * inv + a.eps);
+        // behind the last row 0, so that eps = 0 leaves no 0 / 0 in dw
+        const float r = live ? rsqrtf(sum[0] * inv + a.eps) : 0.f;
         const float m = sum[1] * inv * r;   // mean(dn n)
 #pragma unroll
         for (int v = 0; v < NV; v++) {

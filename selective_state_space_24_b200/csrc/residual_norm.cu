@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
         if (!LAYER)
             sx = s[2];
         const float off = LAYER ? s[2] * inv : 0.f, mg = LAYER ? s[3] * inv : 0.f;
-        const float k = rsqrtf(fmaf(-off, off, s[0] * inv) + a.eps);
+        // behind the last row 0, so that eps = 0 leaves no 0 / 0 in dweight
+        const float k = live ? rsqrtf(fmaf(-off, off, s[0] * inv) + a.eps) : 0.f;
         const float mgy = k * (s[1] * inv - off * mg);   // mean(g y)
 #pragma unroll
         for (int v = 0; v < NV; v++)

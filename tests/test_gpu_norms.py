@@ -162,6 +162,34 @@ def test_norms_repeat_and_capture(cuda_device):
     assert all(torch.equal(c[n], d[n]) for n in c) and torch.equal(y, ssm.gated_norm_fwd(x, w, z=z, group=64))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_no_eps(cuda_device, dtype):
+    """eps = 0, and fewer rows than a block works on at a time."""
+    gen = torch.Generator().manual_seed(6)
+    x, dy, w = r(gen, 3, 64, dtype=dtype), r(gen, 3, 64, dtype=dtype), r(gen, 64)
+    a, b = ob.f64(x, True), ob.f64(w, True)
+    dx, dw = torch.autograd.grad(ob.gated_norm(a, b, eps=0.0), [a, b], dy.double())
+    g = ssm.gated_norm_bwd(x.cuda(), w.cuda(), dy.cuda(), eps=0.0)
+    close(g["dx"], dx)
+    close(g["dweight"], dw, True)
+    for layer in (False, True):
+        dx, dw = torch.autograd.grad(ob.norm(a, b, layer_norm=layer, eps=0.0), [a, b], dy.double())
+        g = ssm.residual_norm_bwd(x.cuda(), x.cuda(), w.cuda(), dy.cuda(), layer_norm=layer, eps=0.0)
+        close(g["dx"], dx)
+        close(g["dweight"], dw, True)
+
+
+def test_more_samples_than_blocks_in_a_column(cuda_device):
+    gen = torch.Generator().manual_seed(7)
+    n = 70000
+    x, dy, w, s = (r(gen, n, 8).cuda(), r(gen, n, 8).cuda(), r(gen, 8).cuda(), r(gen, n, 8).cuda())
+    y, ro = ssm.residual_norm_fwd(x, w, scale=s)
+    assert torch.equal(ro, x * s)
+    zero = torch.zeros_like(w)   # without the norm, the gradients are those of x scale
+    g = ssm.residual_norm_bwd(x, ro, zero, dy, dresidual_out=dy, scale=s)
+    assert torch.equal(g["dx"], dy * s) and torch.equal(g["dscale"], dy * x)
+
+
 def test_empty_rows(cuda_device):
     x, w = torch.zeros(0, 64, device="cuda"), torch.ones(64, device="cuda")
     assert ssm.gated_norm_fwd(x, w).shape == (0, 64)
