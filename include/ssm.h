@@ -517,8 +517,9 @@ SSM_API size_t gdr_chunk_workspace_size(const gdr_dims *dims);
  *   initial_state (B, Hv, V, K) float32 or NULL; may be the same buffer as
  *                 last_state (updated in place)
  *   last_state    (B, Hv, V, K) float32 or NULL: the state after the last step
- * A padded position with dt = 0 and b = 0 (and
- * finite q, k, v) leaves the state as it is.  An empty call (B, L, Hk or Hv
+ * A padded position with dt = 0 and b = 0 (and finite q, k, v) leaves the
+ * state as it is; a position with a large dt (dt A below -104) forgets it, so
+ * several sequences can be packed into one.  An empty call (B, L, Hk or Hv
  * zero) launches no kernel and copies initial_state (or zeros) to last_state.
  */
 SSM_API ssm_status gdr_chunk_fwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state,

@@ -32,7 +32,8 @@ def gdr(q, k, v, delta, A, beta, *, delta_bias=None, delta_softplus=True, beta_s
     q, k = (t.repeat_interleave(Hv // max(Hk, 1), 2) for t in (q * scale, k))
     dt = delta if delta_bias is None else delta + delta_bias
     if delta_softplus:
-        dt = torch.nn.functional.softplus(dt, threshold=1e9)
+        # beyond 100 softplus(x) - x < 4e-44 is nothing in float64; its exp(x) would overflow the derivative
+        dt = torch.nn.functional.softplus(dt, threshold=100)
     b = torch.sigmoid(beta) if beta_sigmoid else beta
     S = torch.zeros(B, Hv, V, K, dtype=q.dtype) if initial_state is None else initial_state
     outs = []

@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
             gl[i] = 0.f;
             s.b[r] = 0.f;
             if (r < w.valid) {
-                gl[i] = gdr_dt(gdr_ld(static_cast<const bf16 *>(a.delta), (w.tok + r) * a.Hv + w.h), bias, a.softplus) * Ah;
+                const float de = gdr_ld(static_cast<const bf16 *>(a.delta), (w.tok + r) * a.Hv + w.h);
+                gl[i] = gdr_log_decay(gdr_dt(de, bias, a.softplus), Ah);
                 const float be = gdr_ld(static_cast<const bf16 *>(a.beta), (w.tok + r) * a.Hv + w.h);
                 s.b[r] = a.sigmoid ? gdr_sigmoid(be) : be;
             }

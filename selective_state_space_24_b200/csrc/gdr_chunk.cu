@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const bool in = c * kC + 2 * lane + e < L;
-                g[e] = in ? gdr_dt(dl[e], bias, a.softplus) * Ah : 0.f;
+                g[e] = in ? gdr_log_decay(gdr_dt(dl[e], bias, a.softplus), Ah) : 0.f;
                 bb[e] = in ? (a.sigmoid ? gdr_sigmoid(be[e]) : be[e]) : 0.f;
             }
             fetch(c + 1);

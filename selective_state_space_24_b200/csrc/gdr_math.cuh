@@ -22,6 +22,16 @@ __device__ __forceinline__ float gdr_dt(float raw, float bias, int softplus)
     const float v = raw + bias;
     return softplus ? softplus_f(v) : v;
 }
+// One step's log2 decay as the chunked kernels add it up.  A float32 decay
+// below 2^-150 is zero, so the logarithm stops there: further out it would
+// cost the sums, from which later steps' decays are differences, their low
+// bits (one step of -1e5 leaves them 2^-8), and an infinite one would leave
+// NaN.  NaN stays NaN.
+__device__ __forceinline__ float gdr_log_decay(float dt, float A_log2e)
+{
+    const float g = dt * A_log2e;
+    return g < -150.f ? -150.f : g;
+}
 // sigmoid(v), also dt's derivative through the softplus
 __device__ __forceinline__ float gdr_sigmoid(float v) { return rcp_mufu(1.f + ex2_mufu(-v * kLog2e)); }
 

@@ -231,7 +231,7 @@ def run_bwd(x, dout, dlast=None, flags={}):
     return g
 
 
-def check_bwd(x, flags, seed=1, dlast=False):
+def check_bwd(x, flags, seed=1, dlast=False, spread=1.0):
     gen = torch.Generator().manual_seed(seed)
     dout = torch.randn(x["v"].shape, generator=gen).to(BF16)
     B, _, Hv, V = x["v"].shape
@@ -248,7 +248,7 @@ def check_bwd(x, flags, seed=1, dlast=False):
     for n in names:
         assert torch.isfinite(g[n]).all(), n
         try:
-            close(g[n], ref[n], g[n].dtype == torch.float32)
+            close(g[n], ref[n], g[n].dtype == torch.float32, spread=spread if g[n].dtype == torch.float32 else 1.0)
         except AssertionError as e:
             raise AssertionError(f"{n}: {e}") from e
 
@@ -264,6 +264,36 @@ def test_backward(cuda_device, size, flags, init):
 @pytest.mark.parametrize("name", ["no decay", "strong decay", "writes all"])
 def test_backward_ranges(cuda_device, name):
     check_bwd(make(1, 150, 1, 2, 128, 128, seed=3, init=True, **HARD[name]), {})
+
+
+def _packed(seed):
+    """Three sequences in one: a step so long that nothing stays starts the second and the third.
+    Log2 decays then reach 2 * 150 within a chunk; each of their sums' up to 7 additions is off by at
+    most half a step there, 2^-16, and a decay is the difference of two: 14 * 2^-16 ln 2 = 1.5e-4
+    relative, 7.4 times the 2e-5 above, on top of it."""
+    x = make(2, 150, 1, 2, 128, 128, seed=seed, init=True)
+    x["delta"][:, [70, 101]] = 1e4
+    return x
+
+
+def test_forward_packed_sequences(cuda_device):
+    x = _packed(8)
+    out, last = run_fwd(x, {})
+    ro, rs = ob.gdr(**f64(x))
+    close(out, ro, False)
+    close(last, rs, True, spread=8.4)
+    own, _ = run_fwd({n: t[:, 101:].contiguous() if isinstance(t, torch.Tensor) and t.dim() > 2 and n != "initial_state"
+                      else t for n, t in x.items()}, {})
+    close(out[:, 101:], own.double().cpu(), False)
+
+
+def test_backward_packed_sequences(cuda_device):
+    x = _packed(9)
+    check_bwd(x, {}, spread=8.4)
+    dout = torch.zeros(x["v"].shape, dtype=BF16)
+    dout[:, 101:] = 1.0
+    g = run_bwd(x, dout)
+    assert not any(g[n][:, :101].any() for n in ("dq", "dk", "dv", "ddelta", "dbeta")) and not g["dinitial_state"].any()
 
 
 def test_backward_repeats(cuda_device):
