@@ -5,8 +5,8 @@ residual_norm_fwd / _bwd (include/ssm.h; names as there).
 Tensors are contiguous, on one CUDA device, which need not be the current
 one; shapes and types are checked before the call.  Work runs on ``stream``
 (default: the current stream of the tensors' device).  What the call
-allocates (results not passed in, the workspace) is kept alive for that
-stream.
+allocates (results not passed in, the workspace) is that stream's memory and
+kept alive for the current stream too.
 """
 from __future__ import annotations
 
@@ -99,7 +99,7 @@ class _Call:
             raise TypeError(f"{name}: unsupported dtype {x.dtype}")
         self.torch, self.f32 = _Torch.torch, _Torch.f32
         self.name, self.device, self.stream = name, x.device, stream
-        self.made = []   # allocated here, to be kept for a stream that is not the current one
+        self.made = []   # allocated on an explicit stream, to be kept for the current one, which will use them
 
     def ptr(self, t, what, shape, dtype):
         """The address of t after its checks (None for None)."""
@@ -116,12 +116,18 @@ class _Call:
         raise ValueError(f"{self.name}: {what} must be contiguous")
 
     def like(self, t):
-        t = _Torch.empty_like(t)
-        self.made.append(t)
-        return t
+        return self.make(_Torch.empty_like, t)
 
     def new(self, shape, dtype):
-        t = self.torch.empty(shape, dtype=dtype, device=self.device)
+        return self.make(self.torch.empty, shape, dtype=dtype, device=self.device)
+
+    def make(self, what, *args, **kw):
+        """what(..) from the memory of the stream that the call runs on, which
+        other streams are done with."""
+        if self.stream is None:
+            return what(*args, **kw)
+        with self.torch.cuda.stream(self.stream):
+            t = what(*args, **kw)
         self.made.append(t)
         return t
 
@@ -148,7 +154,7 @@ class _Call:
         status = fn(*args, s)
         if s != here:
             for t in self.made:
-                t.record_stream(self.stream)
+                t.record_stream(self.torch.cuda.current_stream(self.index))
         if status != 0:
             raise SSMError(status, self.name)
 

@@ -155,6 +155,21 @@ def test_explicit_stream_keeps_its_memory(cuda_device):
             assert torch.equal(g[n], want[n]), n
 
 
+def test_explicit_stream_and_memory_still_in_use(cuda_device):
+    """Memory that the current stream has freed but not finished with is not used on the other stream."""
+    a = _bwd_args(6)
+    want = ssm.gdr_chunk_bwd(*a)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(40_000_000)   # some 20 ms
+    for n in (1 << 18, 1 << 20, 1 << 22, 1 << 24):
+        torch.full((n,), float("nan"), device="cuda")
+    g = ssm.gdr_chunk_bwd(*a, stream=s)
+    torch.cuda.synchronize()
+    for n in g:
+        assert torch.equal(g[n], want[n]), n
+
+
 def test_unit_scale_zero_and_shared_inputs(cuda_device):
     """q and k the same tensor; a zero scale gives zero outputs and finite gradients."""
     a = _bwd_args(5)
