@@ -25,13 +25,34 @@
 // bf16 pairs between them.
 //
 // Per chunk the state's dependence runs S -> S K^T -> (V - ..) -> T .. -> N ->
-// N^T K -> S: four products of the tensor core with a pass of 256 threads
-// after each.  The two halves of S's columns (K = 128) are handed on one by
-// one, so their passes overlap with products.  Beside it, for the chunks
-// ahead, two teams of four warps in turn build P and T from K K^T and Q K^T
-// (one product), a loader brings the tiles of K, Q, V (TMA, three stages) and
-// the log decays, and the outputs of a chunk are read while the next chunk's
-// first product runs.
+// N^T K -> S: three products of the tensor core with a pass of the state's
+// sixteen warps (a lane's row in quarters) after each.  The two halves of S's
+// columns (K = 128) are handed on one by one, so their passes overlap with
+// products.  Beside it, for the chunks ahead, two teams of four warps in turn
+// build P and T from K K^T and Q K^T (one product), one warp brings the tiles
+// of K and Q (TMA, three stages) and the log decays, one those of V, and the
+// outputs of a chunk are read and written while T's product of the next runs.
+//
+// Bound by the latency of that dependence: three products, three passes
+// through tensor memory and the barriers between them, 3.7-3.8 us a chunk,
+// whatever HBM and the tensor cores could do.  So one block of 28 warps per
+// SM, a role each, and nothing but the dependence between two chunks' states.
+// Measured on B200, K = V = 128: 1 x 4096, 32 heads 232 us; 4 x 8192, 32
+// heads (128 blocks for 148 SMs) 540 us after a flush of L2, 482 behind another
+// call, 0.31 of the time of its bytes.  Steps on the way, 4 x 8192: 9650 us on
+// FMA units, 620 with the chain on the tensor cores, 576 with the outputs
+// behind T's product, 540 with the scalars laid out for packed arithmetic and
+// waits that poll less, then K K^T of the chunk after next issued behind T's
+// product.
+//
+// The size of the code counts too.  Seven loops run on an SM at once, and
+// where more than about 14 SMs of a GPC run them their instruction cache
+// misses: 3.7 us a chunk with 112 blocks, 4.7 with 148, a third of the warps'
+// stalls "no instruction".  So what appeared twice appears once and products are
+// issued from loops over 64 columns: 128 blocks 4.16 -> 3.77 us a chunk, 148
+// 4.70 -> 4.15.  (One code for all rows of T saves another 4 KB, 148 blocks
+// 3.80 us, but lengthens T's latency: 128 blocks 3.95; loops of single products
+// issue too slowly: 16 blocks 3.47 -> 3.65.)
 #include <type_traits>
 
 #include "gdr_math.cuh"
@@ -153,7 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, bars.tmem, 0);
     volatile int *abort = &bars.abort;
-    auto wait = [&](uint64_t *bar, uint32_t parity) { return warp_wait(bar, parity, abort, &g_gdr_error); };
+    bool failed = false;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (warp_wait(bar, parity, abort))
+            return true;
+        failed = true;
+        return false;
+    };
     auto stage = [&](int c) { return sm + (c % kKQ) * 4 * kTile; };   // K, Q
     auto vtile = [&](int c) { return sm + kOffV + (c & 1) * 2 * kTile; };
     auto vec = [&](int c) { return reinterpret_cast<Vec *>(sm + kOffVec) + c % kVecs; };
@@ -229,15 +256,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive1(&bars.out[c & 1]);
             return true;
         };
-        bool ok = true;
-        for (int c = 0; c < nch; c++) {
+        for (int c = 0; c <= nch; c++) {
             const Vec *ve = vec(c);
-            ok = false;
+            const bool more = c < nch;   // else only the last chunk's outputs are left
             // 1. diag(b)(V - diag(c) K^ S^T), this half's 32 steps
-            if (!wait(&bars.vfull[c & 1], phase2(c)) || !wait(&bars.ready[c & 1], phase2(c)) || !wait(&bars.ks, c & 1))
+            if (more && (!wait(&bars.vfull[c & 1], phase2(c)) || !wait(&bars.ready[c & 1], phase2(c)) || !wait(&bars.ks, c & 1)))
                 break;
             fence_after();
-            if (live) {
+            if (more && live) {
                 const uint32_t vpitch = 2 * V;
                 const uint8_t *vt = vtile(c) + 16 * quarter * vpitch + 2 * v;
                 uint32_t r[16], hi[8], lo[8];
@@ -258,10 +284,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
             }
             fence_before();
-            arrive1(&bars.d);
+            if (more)
+                arrive1(&bars.d);
             // 2. N for the outputs, N diag(e) for the state (the last chunk's outputs
             // while T's product runs)
-            if ((c > 0 && !outputs(c - 1)) || !wait(&bars.t, c & 1))
+            if ((c > 0 && !outputs(c - 1)) || !more || !wait(&bars.t, c & 1))
                 break;
             fence_after();
             if (live) {
@@ -310,11 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_before();
             arrive1(&bars.s[half]);
-            ok = true;
         }
-        if (ok && nch > 0)
-            outputs(nch - 1);
-        if (live && a.last && !*abort) {
+        if (live && a.last && !failed && !*abort) {
 #pragma unroll
             for (int i = 0; i < KQ; i += 4)
                 *reinterpret_cast<float4 *>(a.last + srow + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
@@ -337,29 +361,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (a.l2norm) {
                 // squares of 16 rows of K and of Q: the diagonal of their products with themselves
+                float acc[2][2][4] = {};
+#pragma unroll 2
+                for (int k = 0; k < kSteps; k++)
 #pragma unroll
-                for (int m = 0; m < 2; m++) {
-                    float acc[2][4] = {};
-#pragma unroll
-                    for (int k = 0; k < kSteps; k++) {
+                    for (int m = 0; m < 2; m++) {
                         uint32_t r[4];
                         ldsm(smem_u32(st) + ((k >> 2) * 2 + m) * kTile +
                                  sw128(16 * pw + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * (k & 3) + (lane >> 4)),
                              r);
-                        mma16816(acc[0], r, r[0], r[2]);
-                        mma16816(acc[1], r, r[1], r[3]);
+                        mma16816(acc[m][0], r, r[0], r[2]);
+                        mma16816(acc[m][1], r, r[1], r[3]);
                     }
-                    if ((lane & 3) == lane >> 3) {   // columns 2 t, 2 t + 1 hold the diagonal of row lane / 4
-                        const int r0 = 16 * pw + (lane >> 2);
-                        const float n0 = rsqrtf(((lane >> 2) & 1 ? acc[0][1] : acc[0][0]) + kL2Eps);
-                        const float n1 = rsqrtf(((lane >> 2) & 1 ? acc[1][3] : acc[1][2]) + kL2Eps);
-                        if (m == 0) {
-                            ve->rk[r0] = n0;
-                            ve->rk[r0 + 8] = n1;
-                        } else {
-                            ve->gq[r0] = n0;
-                            ve->gq[r0 + 8] = n1;
-                        }
+                if ((lane & 3) == lane >> 3) {   // columns 2 t, 2 t + 1 hold the diagonal of row lane / 4
+                    const int r0 = 16 * pw + (lane >> 2);
+#pragma unroll
+                    for (int m = 0; m < 2; m++) {
+                        float *n = m ? ve->gq : ve->rk;
+                        n[r0] = rsqrtf(((lane >> 2) & 1 ? acc[m][0][1] : acc[m][0][0]) + kL2Eps);
+                        n[r0 + 8] = rsqrtf(((lane >> 2) & 1 ? acc[m][1][3] : acc[m][1][2]) + kL2Eps);
                     }
                 }
             } else if (!isq) {
@@ -419,10 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 16; j++)
                         w[j] = j <= n ? w[j] : 0.f;
                 }
-                if (isq) {
-                    put(Pb, p, w);
-                } else if (p < blk) {
-                    put(Tb, p, w);
+                if (isq || p < blk) {
+                    put(isq ? Pb : Tb, p, w);
                 } else if (p == blk) {
 #pragma unroll
                     for (int j = 0; j < 16; j++)
@@ -543,11 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t s = operand(smem_u32(stage(c)));
             if (elect()) {
                 fence_after();
+#pragma unroll 1
+                for (int f = 0; f < K / 64; f++)
 #pragma unroll
-                for (int k = 0; k < kSteps; k++) {
-                    const uint64_t o = s + (((k >> 2) * 2 * kTile + (k & 3) * 32) >> 4);
-                    mma_ss(tm + kColKK, o, o, id64, k > 0);
-                }
+                    for (int k = 0; k < 4; k++) {
+                        const uint64_t o = s + ((f * 2 * kTile + k * 32) >> 4);
+                        mma_ss(tm + kColKK, o, o, id64, f + k > 0);
+                    }
                 commit(&bars.kk[c & 1]);
             }
             __syncwarp();
@@ -569,13 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __all_sync(0xffffffffu, bar_test(&bars.full[c % kKQ], phase(c)) && bar_test(&bars.kkread, (c - 1) & 1)))
                 issue_kk(next_kk++);
         };
-        ok = kk_blocking() && kk_blocking();
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; i++)
+            ok = kk_blocking();
         for (int c = 0; c < nch && ok; c++) {
             const uint64_t s = operand(smem_u32(stage(c)));
             const uint64_t T = operand(smem_u32(sm + kOffT + (c & 1) * 2 * kTile));
             const uint64_t P = operand(smem_u32(sm + kOffP + (c % kP) * 2 * kTile));
             // S K^T (hi + lo), a half of S's columns at a time
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < 2; half++) {
                 ok = wait(&bars.s[half], c & 1);
                 if (!ok)
@@ -583,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (elect()) {
                     fence_after();
 #pragma unroll
-                    for (int k = half * kSteps / 2; k < (half + 1) * kSteps / 2; k++) {
+                    for (int i = 0; i < kSteps / 2; i++) {
+                        const int k = half * (kSteps / 2) + i;
                         const uint64_t kd = s + (((k >> 2) * 2 * kTile + (k & 3) * 32) >> 4);
                         mma_ts(tm + kColKS, tm + kColS + 16 * k, kd, id64, k > 0);
                         mma_ts(tm + kColKS, tm + kColS + 16 * k + 8, kd, id64, true);
@@ -619,12 +642,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (elect()) {
                 fence_after();
+#pragma unroll 1
+                for (int f = 0; f < K / 64; f++)
 #pragma unroll
-                for (int k = 0; k < kSteps; k++) {
-                    const uint64_t qd = s + ((((k >> 2) * 2 + 1) * kTile + (k & 3) * 32) >> 4);
-                    mma_ts(tm + kColQS, tm + kColS + 16 * k, qd, id64, k > 0);
-                    mma_ts(tm + kColQS, tm + kColS + 16 * k + 8, qd, id64, true);
-                }
+                    for (int k = 0; k < 4; k++) {
+                        const uint64_t qd = s + (((f * 2 + 1) * kTile + k * 32) >> 4);
+                        mma_ts(tm + kColQS, tm + kColS + 64 * f + 16 * k, qd, id64, f + k > 0);
+                        mma_ts(tm + kColQS, tm + kColS + 64 * f + 16 * k + 8, qd, id64, true);
+                    }
                 commit(&bars.qs);
             }
             __syncwarp();
@@ -632,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             if (elect()) {
                 fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int f = 0; f < K / 64; f++) {   // 64 columns of N^T diag(e) K^ (hi + lo) in S's place
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
@@ -757,6 +782,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     }
     }
+    if (failed)
+        gave_up(abort, &g_gdr_error);
     fence_before();
     __syncthreads();
     if (warp == 0)

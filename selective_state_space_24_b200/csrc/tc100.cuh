@@ -44,23 +44,27 @@ __device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity) { retur
 constexpr int kWaitLimit = 1 << 20;    // polls of a pipeline wait
 constexpr int kDrainLimit = 1 << 22;   // polls of a wait for this block's own copies and products
 
-// Bounded wait of a whole warp.  On giving up a thread sets *error (the
-// library's word, read by ssm_check_device) and the block's abort word, and
-// every later wait of the block gives up at once: the kernel ends promptly,
-// with wrong values, and says so.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned *error)
+// Bounded wait of a whole warp.  False: it gave up, or found the block's abort
+// word set.  The caller then leaves its loop and calls gave_up, and every later
+// wait of the block gives up at once: the kernel ends promptly, with wrong
+// values, and says so.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
     const uint32_t b = smem_u32(bar);
 #pragma unroll 1
     for (int it = 0; it < kWaitLimit; it++) {   // each test waits a while by itself
         if (__all_sync(0xffffffffu, bar_test(b, parity)))
             return true;
-        if ((it & 63) == 63 && __any_sync(0xffffffffu, *abort))
+        if (__any_sync(0xffffffffu, *abort))
             return false;
     }
+    return false;
+}
+// Sets the block's abort word and *error (the library's word, read by ssm_check_device).
+__device__ __forceinline__ void gave_up(volatile int *abort, unsigned *error)
+{
     *abort = 1;
     atomicExch(error, 1u);
-    return false;
 }
 // Wait at the end for work that completes by itself (loads landing, products
 // retiring); it ignores the abort word.
