@@ -46,7 +46,12 @@
  *    for SSM_F32 and of 8 for SSM_BF16.  Otherwise SSM_ERR_MISALIGNED.
  *  - out must not overlap any input.  last_state is written, not accumulated.
  *  - All arithmetic is float32 (the state, dt, exp(dt*A)); bf16 inputs are
- *    widened exactly and the output is rounded to nearest even.
+ *    widened exactly and the output is rounded to nearest even.  Where a
+ *    matrix product on the tensor cores stands for it (ssd_chunk_*, gdr_chunk_*),
+ *    sums and states are float32 and what enters a product is rounded or split
+ *    as its kernel's source says.
+ *  - A workspace serves one call at a time: calls that may overlap (on two
+ *    streams, in two graphs) need one each.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream) and thread-safe.  All arguments are validated before
  *    anything is launched; on an error nothing is launched and the return
@@ -659,7 +664,7 @@ SSM_API ssm_status residual_norm_bwd(const norm_dims *dims, const residual_norm_
 
 /*
  * Waits for `stream`, then reports (and clears) the library's device-side
- * error words: SSM_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel gave
+ * error words (ssd_chunk_fwd, gdr_chunk_fwd and the ordered scans have them): SSM_ERR_DEVICE_TIMEOUT if a bounded wait inside a kernel gave
  * up since the last check, SSM_ERR_INVALID_ARG if a scan order held an
  * index outside [0, L), SSM_ERR_CUDA if the stream reports a CUDA error,
  * SSM_OK otherwise.  Blocking; meant for tests and debugging.

@@ -13,6 +13,13 @@
 // meets (NormPlan), so the weights are read once per thread and dw gathers in
 // registers; each block then writes one partial row of dw, summed by a second
 // small kernel in a fixed order (no atomics: the same bits every time).
+//
+// Measured on B200, bf16: forward, 262144 rows of 128 with a gate 38.5 us
+// (5.2 TB/s, 0.80 of a copy; what is missing are the rows' start and the
+// sum's round trip per row).  Backward, 16384 rows of 2048: 80 us (4.2 TB/s,
+// 0.64): a row's five operands are unpacked, gated and packed at about 14
+// instructions an element, and the row's sum joins eight warps at a barrier,
+// which four blocks of 256 threads per SM cover in part.
 #include "norm_common.cuh"
 
 namespace ssm {

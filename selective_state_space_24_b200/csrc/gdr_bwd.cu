@@ -32,8 +32,25 @@
 // tf32 (11 bits each), and a product is hi hi + hi lo + lo hi; K, Q, V and dO
 // as they came are bf16 and exact in hi alone.  What only reaches bf16
 // results (dP, dA times K and Q) takes one tf32 part; K K^T and Q K^T are bf16
-// products.  (Pairs of bf16 leave dA up to
-// 3e-5 off where the terms cancel.)
+// products.  (Pairs of bf16 leave dA up to 3e-5 off where the terms cancel.)
+//
+// Three launches and a small sum: 1 prepares every chunk by itself, 2 and 3 walk
+// the chunks with 32 state rows a block, forward and in reverse side by side on
+// an SM, 4 takes every chunk by itself again.  What passes between them (T, W,
+// U, P^T dO, the states: 280 KB a chunk and head for K = V = 128) goes through
+// the workspace in float32.
+//
+// Bound by mma.sync (tf32 takes 8 clocks an instruction and SM quarter, three
+// per two-part product) and the instructions that feed it: in the chains the
+// tensor pipe is 41% busy and 52% of the issue slots are taken on average, 56%
+// and 70% on the SMs with two blocks; HBM 13%.  Measured on B200, 2 x 2048, 8 key and 16 value heads,
+// K = V = 128: 703 us (preparation 85, the chains 296, the gradients 328, the sum
+// 4); 2 x 197, 6 heads of 64: 59 us, the latency of four launches.  On the way:
+// 3780 us with FMA units, 890 with two-part tf32, 756 with the parts taken by
+// integer operations instead of cvt.tf32 (4 clocks against 2), 711 with two
+// preparation blocks per SM, 703 (and 72 -> 59 us) with the chains together: by
+// themselves, with two buffers a tile, they took 135 and 174 us.  512 threads
+// a block for the gradients were slower (registers).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

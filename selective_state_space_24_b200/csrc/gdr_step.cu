@@ -11,6 +11,10 @@
 // contiguous bytes a row); all rows are loaded before anything else.  The
 // 2 kRows row sums go through a butterfly that halves the values at each
 // exchange (16 shuffles for 16 sums instead of 80).
+//
+// Measured on B200, K = V = 128, 32 heads, bf16: batch 256 160-165 us, 1.08 GB
+// of states and operands at 6.6 TB/s, the rate of a copy; batch 1 4 us on the
+// device, of some 14 us a call.  A sequence costs 0.54 us a step.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

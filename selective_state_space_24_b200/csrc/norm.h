@@ -9,10 +9,10 @@ namespace ssm {
 
 // How threads cover rows (of one group of columns): tpr threads per row, a
 // power of two, each holding `elems` elements; a block works on threads / tpr
-// rows at a time.  Block b owns the columns of group b % G and walks rows with a stride, so a thread's
-// columns never change: its weights stay in registers and column sums gather
-// there.  Several blocks share the rows of one group (or sample), each
-// with a partial sum of its own.
+// rows at a time.  Block b owns the columns of group b % G and walks rows
+// with a stride, so a thread's columns never change: its weights stay in
+// registers and column sums gather there.  Several blocks share the rows of
+// one group (or sample), each with a partial sum of its own.
 struct NormPlan {
     int elems, tpr, threads;
     int rows_at_once;   // rows a block works on at a time

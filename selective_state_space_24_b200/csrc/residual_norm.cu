@@ -14,6 +14,13 @@
 // dependent sums (the mean is taken before the squares, which keeps the
 // variance exact for rows far from zero).  Thread layout and column sums as
 // in gated_norm.cu; with a scale per sample a block's rows are of one sample.
+// residual_out is rounded once to its type and the norm reads that value, so
+// the backward pass, which gets residual_out, differentiates what was computed.
+//
+// Measured on B200: forward, 16 rows of 1024 (a decode batch) 15.5 us a call,
+// launch and host; 12608 rows of 384 17 us.  Backward of 16384
+// rows of 1024 with post-norm and scale 82 us (3.7 TB/s, 0.56 of a copy): three dependent row
+// sums, each a barrier of the row's warps, between a row's loads and stores.
 #include <type_traits>
 
 #include "norm_common.cuh"
