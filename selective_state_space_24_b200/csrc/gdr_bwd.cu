@@ -44,13 +44,15 @@
 // per two-part product) and the instructions that feed it: in the chains the
 // tensor pipe is 41% busy and 52% of the issue slots are taken on average, 56%
 // and 70% on the SMs with two blocks; HBM 13%.  Measured on B200, 2 x 2048, 8 key and 16 value heads,
-// K = V = 128: 703 us (preparation 85, the chains 296, the gradients 328, the sum
-// 4); 2 x 197, 6 heads of 64: 59 us, the latency of four launches.  On the way:
+// K = V = 128: 666 us (preparation 85, the chains 299, the gradients 290, the sum
+// 4); 2 x 197, 6 heads of 64: 58 us, the latency of four launches.  On the way:
 // 3780 us with FMA units, 890 with two-part tf32, 756 with the parts taken by
 // integer operations instead of cvt.tf32 (4 clocks against 2), 711 with two
 // preparation blocks per SM, 703 (and 72 -> 59 us) with the chains together: by
-// themselves, with two buffers a tile, they took 135 and 174 us.  512 threads
-// a block for the gradients were slower (registers).
+// themselves, with two buffers a tile, they took 135 and 174 us; 666 with V,
+// delta and the second reading of S0 brought in by asynchronous copies ahead of
+// their use in the gradients.  512 threads a block for the gradients were slower
+// (registers), the next head's tiles brought into L2 ahead no faster.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -719,11 +721,11 @@ template <int K> __global__ void __launch_bounds__(kThreads, 2) chains_kernel(co
 
 // ---- 4. per chunk and key head: every gradient
 template <int K, int V> struct GradSmem {
-    bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(V)];
+    bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(V)], v[kC * ph(V)];
     float n[kC * pr(V)], r[kC * pr(V)], x[kC * kPX];
     float t[kC * kPX], m[2][kSlice * pc(K)];   // T; 32 rows of a state, the next 32
     float cs[4 * kC], brk[kC];   // cs, b, rk, rq as in the workspace; b rk
-    float dcs[kC], sum[6][4][kC], red[8];   // sum: row sums of each column of warps
+    float delta[kC], dcs[kC], sum[6][4][kC], red[8];   // sum: row sums of each column of warps
 };
 template <int K, int V>
 __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, const Layout lay, float *partial)
@@ -770,19 +772,26 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         const int64_t bh = b * a.Hv + h;
         const float *ws = static_cast<const float *>(a.workspace) + lay.base(bh, n);
         const float *S0 = ws + lay.S0(), *dS = ws + lay.dS();
-        const bf16 *vp = static_cast<const bf16 *>(a.v) + (tok * a.Hv + h) * V;
         __syncthreads();
         s.cs[threadIdx.x] = ws[threadIdx.x];
+        if (threadIdx.x < valid)
+            s.delta[threadIdx.x] = gdr_ld(static_cast<const bf16 *>(a.delta), (tok + threadIdx.x) * a.Hv + h);
         load_rows<V>(s.o, static_cast<const bf16 *>(ga.dout) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid);
+        load_rows<V>(s.v, static_cast<const bf16 *>(a.v) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid);
         load_f<kC, V>(s.n, ws + lay.U(), pr(V));
         load_f<kC, V>(s.r, ws + lay.dN(), pr(V));
         load_f<kC, kC>(s.t, ws + lay.T(), kPX);
         cp_commit();
-        // S0 and then dS1, 32 rows at a time, two pieces on their way
+        // S0 and then dS1, 32 rows at a time, two pieces on their way; beside
+        // dS1's those of S0 again, in the places of T and R', done with by then
         constexpr int kPieces = V / kSlice;
+        static_assert(kPieces % 2 == 0 && sizeof(s.t) >= sizeof(s.m[0]) && sizeof(s.r) >= sizeof(s.m[0]), "room for a piece");
+        auto beside = [&](int i) { return i & 1 ? s.r : s.t; };
         auto fetch = [&](int i) {
             if (i < 2 * kPieces)
                 load_f<kSlice, K>(s.m[i & 1], (i < kPieces ? S0 : dS - (size_t)V * K) + (size_t)i * kSlice * K, pc(K));
+            if (i >= kPieces && i < 2 * kPieces)
+                load_f<kSlice, K>(beside(i), S0 + (size_t)(i - kPieces) * kSlice * K, pc(K));
             cp_commit();
         };
         fetch(0);
@@ -809,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
                         const float x = r[m][q][2 * e], y = r[m][q][2 * e + 1];
                         st2(&s.r[i * pr(V) + j], x, y);
                         if (i < valid) {
-                            const __nv_bfloat162 vv = *reinterpret_cast<const __nv_bfloat162 *>(vp + (size_t)i * a.Hv * V + j);
+                            const __nv_bfloat162 vv = *reinterpret_cast<const __nv_bfloat162 *>(&s.v[i * ph(V) + j]);
                             dbr[2 * m + e] = fmaf(x, __low2float(vv), fmaf(y, __high2float(vv), dbr[2 * m + e]));
                             *reinterpret_cast<__nv_bfloat162 *>(static_cast<bf16 *>(ga.dv) + ((tok + i) * a.Hv + h) * V + j) =
                                 __floats2bfloat162_rn(bb[i] * x, bb[i] * y);
@@ -931,8 +940,9 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             __syncthreads();
             mm<kTwo, kTwo>(Y, m0, nK, kSlice, RowF{s.n + v0, pr(V)}, ColF{St, pc(K)});
             for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4) {   // c_end <dS1, S0>
-                const float4 f = *reinterpret_cast<const float4 *>(S0 + (size_t)v0 * K + x);
-                const float4 d = *reinterpret_cast<const float4 *>(&St[(x / K) * pc(K) + x % K]);
+                const int at = (x / K) * pc(K) + x % K;
+                const float4 f = *reinterpret_cast<const float4 *>(&beside(i)[at]);
+                const float4 d = *reinterpret_cast<const float4 *>(&St[at]);
                 through = fmaf(dec * d.x, f.x, fmaf(dec * d.y, f.y, fmaf(dec * d.z, f.z, fmaf(dec * d.w, f.w, through))));
             }
             __syncthreads();
@@ -988,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
                 const int row = 2 * lane + i;
                 if (row < valid) {
                     const size_t at = (tok + row) * a.Hv + h;
-                    const float pre = gdr_ld(static_cast<const bf16 *>(a.delta), at);
+                    const float pre = s.delta[row];
                     sA = fmaf(dg[i], gdr_dt(pre, bias, a.softplus), sA);
                     const float dd = dg[i] * Ah * (a.softplus ? gdr_sigmoid(pre + bias) : 1.f);
                     sb += dd;
