@@ -526,6 +526,8 @@ SSM_API size_t gdr_chunk_workspace_size(const gdr_dims *dims);
  * state as it is; a position with a large dt (dt A below -104) forgets it, so
  * several sequences can be packed into one.  An empty call (B, L, Hk or Hv
  * zero) launches no kernel and copies initial_state (or zeros) to last_state.
+ * A NaN or infinity in a row of q, k or v makes its head's outputs undefined
+ * from the start of the row's chunk on: fill the padding.
  */
 SSM_API ssm_status gdr_chunk_fwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state,
                                  void *out, float *last_state, void *workspace, size_t workspace_bytes,
@@ -559,8 +561,10 @@ SSM_API size_t gdr_chunk_bwd_workspace_size(const gdr_dims *dims);
  * Gradients of gdr_chunk_fwd for incoming gradients of out (dout, (B, L, Hv,
  * V) dtype, required) and of last_state (dlast_state, (B, Hv, V, K) float32
  * or NULL).  The states are recomputed, so nothing from the forward call is
- * needed.  Every gradient is written, not accumulated, and sums in a fixed
- * order: the same call gives the same bits.
+ * needed (but a workspace of about 4 KB per step and value head, K = V = 128).
+ * Every gradient is written, not accumulated, and summed in a fixed order: the
+ * same call gives the same bits.  initial_state NULL means zero.  An empty
+ * call writes zeros, and dlast_state to dinitial_state.
  */
 SSM_API ssm_status gdr_chunk_bwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state,
                                  const void *dout, const float *dlast_state, const gdr_grads *grads,

@@ -258,6 +258,10 @@ ssm_status gdr_chunk_bwd(const gdr_dims *dims, const gdr_inputs *in, const float
         if ((s = zero_f32(grads->dA, dims->nheads_v, st)) != SSM_OK ||
             (s = zero_f32(grads->ddelta_bias, dims->nheads_v, st)) != SSM_OK)
             return s;
+        const size_t qk = (size_t)dims->batch * dims->seqlen * dims->nheads_k * dims->headdim_k / 2;   // in floats
+        if ((s = zero_f32(static_cast<float *>(grads->dq), qk, st)) != SSM_OK ||
+            (s = zero_f32(static_cast<float *>(grads->dk), qk, st)) != SSM_OK)
+            return s;
         return pass_state(dims, dlast_state, grads->dinitial_state, st);
     }
     if ((s = check_gdr_inputs(in)) != SSM_OK)

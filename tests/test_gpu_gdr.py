@@ -183,6 +183,12 @@ def test_empty_calls(cuda_device):
     assert not g["dA"].any() and not g["ddelta_bias"].any() and bool((g["dinitial_state"] == 1).all())
 
 
+def test_no_value_heads(cuda_device):
+    x = make(2, 70, 2, 0, 64, 64)
+    g = run_bwd(x, torch.zeros(2, 70, 0, 64, dtype=BF16))
+    assert g["dq"].shape == (2, 70, 2, 64) and not g["dq"].any() and not g["dk"].any()
+
+
 def test_state_and_streams(cuda_device):
     """Another stream, and a captured call replayed on new inputs."""
     x = cuda(make(1, 150, 2, 2, 64, 64, seed=9))
