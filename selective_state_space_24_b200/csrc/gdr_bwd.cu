@@ -37,7 +37,7 @@
 // Three launches and a small sum: 1 prepares every chunk by itself, 2 and 3 walk
 // the chunks with 32 state rows a block, forward and in reverse side by side on
 // an SM, 4 takes every chunk by itself again.  What passes between them (T, W,
-// U, P^T dO, the states: 280 KB a chunk and head for K = V = 128) goes through
+// U, P^T dO, the states: 250 KB a chunk and head for K = V = 128) goes through
 // the workspace in float32.
 //
 // Bound by mma.sync (tf32 takes 8 clocks an instruction and SM quarter, three
