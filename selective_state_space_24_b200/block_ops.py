@@ -115,21 +115,23 @@ class _Call:
             raise ValueError(f"{self.name}: {what} must be on {self.device}, got {t.device}")
         raise ValueError(f"{self.name}: {what} must be contiguous")
 
+    # Memory is the stream's that the call runs on: other streams are done with it.
+
     def like(self, t):
-        return self.make(_Torch.empty_like, t)
-
-    def new(self, shape, dtype):
-        return self.make(self.torch.empty, shape, dtype=dtype, device=self.device)
-
-    def make(self, what, *args, **kw):
-        """what(..) from the memory of the stream that the call runs on, which
-        other streams are done with."""
         if self.stream is None:
-            return what(*args, **kw)
+            return _Torch.empty_like(t)
         with self.torch.cuda.stream(self.stream):
-            t = what(*args, **kw)
+            t = _Torch.empty_like(t)
         self.made.append(t)
         return t
+
+    def new(self, shape, dtype):
+        if self.stream is not None:
+            with self.torch.cuda.stream(self.stream):
+                t = self.torch.empty(shape, dtype=dtype, device=self.device)
+            self.made.append(t)
+            return t
+        return self.torch.empty(shape, dtype=dtype, device=self.device)
 
     def workspace(self, need, ws):
         """(address, bytes) of a workspace of at least `need` bytes."""

@@ -178,3 +178,68 @@ def test_unit_scale_zero_and_shared_inputs(cuda_device):
     assert not o.any()
     g = ssm.gdr_chunk_bwd(*a, scale=0.0)
     assert not g["dq"].any() and all(bool(torch.isfinite(t).all()) for t in g.values())
+
+
+# ---- more than 2^31 elements: the last part against a call of its own
+
+def _tail(x, lo, hi):
+    return x[lo:hi].clone()   # not a view: a state is updated in place
+
+
+def test_long_sequences_beyond_32_bit_offsets(cuda_device):
+    B, L, Hk, Hv, K, V = 3, 64 * 2750, 1, 64, 64, 64   # v: 2.16e9 elements
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF16)   # noqa: E731
+    x = [r(B, L, Hk, K), r(B, L, Hk, K), r(B, L, Hv, V), r(B, L, Hv), -1 - torch.rand(Hv, device="cuda", generator=gen),
+         r(B, L, Hv)]
+    assert x[2].numel() > 2 ** 31
+    last = torch.empty(B, Hv, V, K, device="cuda")
+    out = ssm.gdr_chunk_fwd(*x, last_state=last)
+    own = torch.empty(1, Hv, V, K, device="cuda")
+    want = ssm.gdr_chunk_fwd(*(t if t.dim() == 1 else _tail(t, B - 1, B) for t in x), last_state=own)
+    assert torch.equal(out[B - 1:], want) and torch.equal(last[B - 1:], own)
+    ssm.check_device()
+
+
+def test_backward_workspace_beyond_32_bit_offsets(cuda_device):
+    B, L, Hk, Hv, K, V = 3, 64 * 800, 2, 16, 128, 128   # 38400 chunks and heads of 61,696 floats
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF16)   # noqa: E731
+    x = [r(B, L, Hk, K), r(B, L, Hk, K), r(B, L, Hv, V), r(B, L, Hv), -1 - torch.rand(Hv, device="cuda", generator=gen),
+         r(B, L, Hv), r(B, L, Hv, V)]
+    g = ssm.gdr_chunk_bwd(*x)
+    w = ssm.gdr_chunk_bwd(*(t if t.dim() == 1 else _tail(t, B - 1, B) for t in x))
+    for n in ("dq", "dk", "dv", "ddelta", "dbeta"):
+        assert torch.equal(g[n][B - 1:], w[n]), n
+
+
+def test_states_beyond_32_bit_offsets(cuda_device):
+    B, Hk, Hv, K, V = 1040, 8, 128, 128, 128   # 2.18e9 state elements
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF16)   # noqa: E731
+    x = [r(B, Hk, K), r(B, Hk, K), r(B, Hv, V), r(B, Hv), -torch.ones(Hv, device="cuda"), r(B, Hv)]
+    state = torch.randn(B, Hv, V, K, generator=gen, device="cuda")
+    own = _tail(state, B - 8, B)
+    out = ssm.gdr_step(*x, state)
+    want = ssm.gdr_step(*(t if t.dim() == 1 else _tail(t, B - 8, B) for t in x), own)
+    assert torch.equal(out[B - 8:], want) and torch.equal(state[B - 8:], own)
+
+
+def test_norms_beyond_32_bit_offsets(cuda_device):
+    rows, dim = (1 << 20) + 64, 2048
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    x = torch.randn(rows, dim, generator=gen, device="cuda", dtype=BF16)
+    w = torch.rand(dim, device="cuda") + 0.5
+    z, end = x.flip(1), slice(rows - 64, rows)
+    y = ssm.gated_norm_fwd(x, w, z=z, group=256)
+    assert torch.equal(y[end], ssm.gated_norm_fwd(x[end].contiguous(), w, z=z[end].contiguous(), group=256))
+    g = ssm.gated_norm_bwd(x, w, y, z=z, group=256)
+    own = ssm.gated_norm_bwd(x[end].contiguous(), w, y[end].contiguous(), z=z[end].contiguous(), group=256)
+    assert torch.equal(g["dx"][end], own["dx"]) and torch.equal(g["dz"][end], own["dz"])
+    del g, z
+    y, ro = ssm.residual_norm_fwd(x, w, layer_norm=True)
+    y2, ro2 = ssm.residual_norm_fwd(x[end].contiguous(), w, layer_norm=True)
+    assert torch.equal(y[end], y2) and torch.equal(ro[end], ro2)
+    g = ssm.residual_norm_bwd(x, ro, w, y, layer_norm=True)
+    own = ssm.residual_norm_bwd(x[end].contiguous(), ro2, w, y2, layer_norm=True)
+    assert torch.equal(g["dx"][end], own["dx"]) and torch.equal(g["dresidual"][end], own["dresidual"])
