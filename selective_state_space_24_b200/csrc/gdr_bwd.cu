@@ -69,16 +69,19 @@ constexpr int kSlice = 32;     // state rows of one chain block
 
 using bf16 = __nv_bfloat16;
 
+constexpr int kScalars = 5;
 // What one (chunk, value head) keeps in the workspace, in floats.
 struct Layout {
     int K, V, NC;
     int64_t heads;   // B Hv
     __host__ __device__ size_t per() const { return dS() + (size_t)V * K; }
     __host__ __device__ size_t base(int64_t bh, int n) const { return ((size_t)bh * NC + n) * per(); }
-    __host__ __device__ size_t cs() const { return 0; }       // log decays (base 2), summed; then b
+    // five scalars a step: log decays (base 2), summed, as hi, b, factors of a row of k and of q, and lo
+    __host__ __device__ size_t cs() const { return 0; }
     __host__ __device__ size_t rk() const { return 2 * kC; }  // factor of a row of k
     __host__ __device__ size_t rq() const { return 3 * kC; }  // and of q (scale in it)
-    __host__ __device__ size_t T() const { return 4 * kC; }
+    __host__ __device__ size_t cl() const { return 4 * kC; }
+    __host__ __device__ size_t T() const { return kScalars * kC; }
     __host__ __device__ size_t W() const { return T() + kC * kC; }
     __host__ __device__ size_t U() const { return W() + (size_t)kC * K; }    // T diag(b) V, then N
     __host__ __device__ size_t dN() const { return U() + (size_t)kC * V; }   // P^T dO, then dN
@@ -337,7 +340,7 @@ template <int ROWS, int N> __device__ __forceinline__ void load_f(float *dst, co
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + (size_t)r * N + c) : "memory");
     }
 }
-// 64 rows of `kSlice` floats, ld apart, and the four scalars of every step
+// 64 rows of `kSlice` floats, ld apart, and the scalars of every step
 __device__ __forceinline__ void load_slice(float *dst, const float *src, int ld)
 {
     for (int x = threadIdx.x; x < kC * kSlice / 4; x += kThreads) {
@@ -348,7 +351,8 @@ __device__ __forceinline__ void load_slice(float *dst, const float *src, int ld)
 }
 __device__ __forceinline__ void load_scalars(float *dst, const float *src)
 {
-    if (threadIdx.x < kC) {
+    static_assert(kScalars * kC / 4 <= kThreads, "16 bytes a thread");
+    if (threadIdx.x < kScalars * kC / 4) {
         const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + 4 * threadIdx.x);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + 4 * threadIdx.x) : "memory");
     }
@@ -384,7 +388,7 @@ template <int K, int V> struct PrepSmem {
         float p[kC * kPX];
     };
     float a[kC * kPX], t[kC * kPX];
-    float cs[kC], b[kC], rk[kC], rq[kC], wf[kC];   // wf: b c / |k|
+    float cs[kC], cl[kC], b[kC], rk[kC], rq[kC], wf[kC];   // wf: b c / |k|
 };
 template <int K, int V>
 __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, const Layout lay)
@@ -415,14 +419,12 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
                 s.b[r] = a.sigmoid ? gdr_sigmoid(be) : be;
             }
         }
-        float incl = gl[0] + gl[1];
-        for (int o = 1; o < 32; o <<= 1) {
-            const float v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o)
-                incl += v;
+        float2 sum[2];
+        gdr_log_sums(gl, sum);
+        for (int i = 0; i < 2; i++) {
+            s.cs[2 * lane + i] = sum[i].x;
+            s.cl[2 * lane + i] = sum[i].y;
         }
-        s.cs[2 * lane] = incl - gl[1];
-        s.cs[2 * lane + 1] = incl;
     }
     cp_wait<0>();
     __syncthreads();
@@ -451,11 +453,11 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
         mm16(qk, m0, 16 * wn, K, s.q, ph(K), s.k, ph(K));
         __syncthreads();   // Q is done with
         each(kk, m0, 16 * wn, [&](int i, int j, float v) {
-            s.a[i * kPX + j] = j < i ? s.b[i] * ex2_mufu(s.cs[i] - s.cs[j]) * s.rk[i] * s.rk[j] * v : 0.f;
+            s.a[i * kPX + j] = j < i ? s.b[i] * gdr_between(s.cs[i], s.cl[i], s.cs[j], s.cl[j]) * s.rk[i] * s.rk[j] * v : 0.f;
             s.t[i * kPX + j] = 0.f;
         });
         each(qk, m0, 16 * wn, [&](int i, int j, float v) {
-            s.p[i * kPX + j] = j <= i ? ex2_mufu(s.cs[i] - s.cs[j]) * s.rq[i] * s.rk[j] * v : 0.f;
+            s.p[i * kPX + j] = j <= i ? gdr_between(s.cs[i], s.cl[i], s.cs[j], s.cl[j]) * s.rq[i] * s.rk[j] * v : 0.f;
         });
     }
     __syncthreads();
@@ -523,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
         const int i = threadIdx.x;
         ws[lay.cs() + i] = s.cs[i];
         ws[lay.cs() + kC + i] = s.b[i];
+        ws[lay.cl() + i] = s.cl[i];
         ws[lay.rk() + i] = s.rk[i];
         ws[lay.rq() + i] = s.rq[i];
     }
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
 template <int K> struct ChainSmem {
     float w[kC * pr(K)];
     bf16 k[kC * ph(K)];
-    float u[kC * kPN], v[4 * kC];   // U; cs, b, 1 / |k|, scale / |q|
+    float u[kC * kPN], v[kScalars * kC];   // U; cs, b, 1 / |k|, scale / |q|, cs's lo
     float s[kSlice * pr(K)], n[kC * kPN];
 };
 template <int K> __device__ __forceinline__ void forward_chain(const GdrArgs &a, const Layout &lay, ChainSmem<K> &s, int64_t bh, int v0)
@@ -584,14 +587,15 @@ template <int K> __device__ __forceinline__ void forward_chain(const GdrArgs &a,
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
             *reinterpret_cast<float4 *>(ws + lay.S0() + (size_t)v0 * K + x) =
                 *reinterpret_cast<const float4 *>(&s.s[(x / K) * pr(K) + x % K]);
-        const float *cs = s.v, *rk = s.v + 2 * kC;
-        const float end = cs[kC - 1], dec = ex2_mufu(end);
+        const float *cs = s.v, *rk = s.v + 2 * kC, *cl = s.v + 4 * kC;
+        const float end = cs[kC - 1], endl = cl[kC - 1], dec = ex2_mufu(end);
         float acc[1][2][4];
         zero(acc);
         mm<kTwo, kTwo>(acc, mN, nN, K, RowF{s.w, pr(K)}, RowF{s.s, pr(K)});
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
-            const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
+            const float e[2] = {rk[i0] * gdr_between(end, endl, cs[i0], cl[i0]),
+                                rk[i0 + 8] * gdr_between(end, endl, cs[i0 + 8], cl[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
                 const float2 u = *reinterpret_cast<const float2 *>(&s.u[i * kPN + j]);
                 x = u.x - x, y = u.y - y;
@@ -619,7 +623,7 @@ template <int K> __device__ __forceinline__ void forward_chain(const GdrArgs &a,
 template <int K> struct ReverseSmem {
     float w[kC * pc(K)];
     bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(kSlice)];
-    float u[kC * kPN], v[4 * kC];   // P^T dO; scalars
+    float u[kC * kPN], v[kScalars * kC];   // P^T dO; scalars
     float g[kSlice * pr(K)], n[kC * kPN];
     float f[kC];
 };
@@ -658,8 +662,8 @@ template <int K> __device__ __forceinline__ void reverse_chain(const GdrBwdArgs 
         float *ws = base + lay.base(bh, n);
         cp_wait<1>();
         __syncthreads();
-        const float *cs = s.v, *rk = s.v + 2 * kC, *rq = s.v + 3 * kC;
-        const float end = cs[kC - 1], dec = ex2_mufu(end);
+        const float *cs = s.v, *rk = s.v + 2 * kC, *rq = s.v + 3 * kC, *cl = s.v + 4 * kC;
+        const float end = cs[kC - 1], endl = cl[kC - 1], dec = ex2_mufu(end);
         if (threadIdx.x < kC)
             s.f[threadIdx.x] = rq[threadIdx.x] * ex2_mufu(cs[threadIdx.x]);
         for (int x = threadIdx.x * 4; x < kSlice * K; x += kThreads * 4)
@@ -670,7 +674,8 @@ template <int K> __device__ __forceinline__ void reverse_chain(const GdrBwdArgs 
         mm<kExact, kTwo>(acc, mN, nN, K, RowH{s.k, ph(K)}, RowF{s.g, pr(K)});
         {
             const int i0 = mN + ((threadIdx.x & 31) >> 2);
-            const float e[2] = {rk[i0] * ex2_mufu(end - cs[i0]), rk[i0 + 8] * ex2_mufu(end - cs[i0 + 8])};
+            const float e[2] = {rk[i0] * gdr_between(end, endl, cs[i0], cl[i0]),
+                                rk[i0 + 8] * gdr_between(end, endl, cs[i0 + 8], cl[i0 + 8])};
             pairs(acc, mN, nN, [&](int i, int j, float x, float y) {
                 const float2 u = *reinterpret_cast<const float2 *>(&s.u[i * kPN + j]);
                 const float f = e[(i - i0) >> 3];
@@ -724,7 +729,7 @@ template <int K, int V> struct GradSmem {
     bf16 k[kC * ph(K)], q[kC * ph(K)], o[kC * ph(V)], v[kC * ph(V)];
     float n[kC * pr(V)], r[kC * pr(V)], x[kC * kPX];
     float t[kC * kPX], m[2][kSlice * pc(K)];   // T; 32 rows of a state, the next 32
-    float cs[4 * kC], brk[kC];   // cs, b, rk, rq as in the workspace; b rk
+    float cs[kScalars * kC], brk[kC];   // cs, b, rk, rq, cs's lo as in the workspace; b rk
     float delta[kC], dcs[kC], sum[6][4][kC], red[8];   // sum: row sums of each column of warps
 };
 template <int K, int V>
@@ -739,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
     const int n = blockIdx.x % lay.NC;
     const int64_t b = bhk / a.Hk;
     const int hk = (int)(bhk % a.Hk);
-    const float *cs = s.cs, *bb = s.cs + kC, *rk = s.cs + 2 * kC, *rq = s.cs + 3 * kC;
+    const float *cs = s.cs, *bb = s.cs + kC, *rk = s.cs + 2 * kC, *rq = s.cs + 3 * kC, *cl = s.cs + 4 * kC;
     const int t0 = n * kC, valid = a.L - t0 < kC ? a.L - t0 : kC;
     const size_t tok = (size_t)b * a.L + t0;
     const int m0 = 32 * (warp >> 2), wn = warp & 3, gq = lane >> 2, tq = lane & 3;
@@ -773,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         const float *ws = static_cast<const float *>(a.workspace) + lay.base(bh, n);
         const float *S0 = ws + lay.S0(), *dS = ws + lay.dS();
         __syncthreads();
-        s.cs[threadIdx.x] = ws[threadIdx.x];
+        for (int x = threadIdx.x; x < kScalars * kC; x += kThreads)
+            s.cs[x] = ws[x];
         if (threadIdx.x < valid)
             s.delta[threadIdx.x] = gdr_ld(static_cast<const bf16 *>(a.delta), (tok + threadIdx.x) * a.Hv + h);
         load_rows<V>(s.o, static_cast<const bf16 *>(ga.dout) + (tok * a.Hv + h) * V, (size_t)a.Hv * V, valid);
@@ -800,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         __syncthreads();
         if (threadIdx.x < kC)   // read much later
             s.brk[threadIdx.x] = bb[threadIdx.x] * rk[threadIdx.x];
-        const float end = cs[kC - 1];
+        const float end = cs[kC - 1], endl = cl[kC - 1];
         // R' = T^T dN
         {
             float r[2][NV][4];
@@ -834,8 +840,17 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             zero(xp);
             mm<kTwo, kTwo>(xa, m0, nC, V, RowF{s.r, pr(V)}, RowF{s.n, pr(V)});
             mm<kExact, kTwo>(xp, m0, nC, V, RowH{s.o, ph(V)}, RowF{s.n, pr(V)});
-            each(xa, m0, nC, [&](int i, int j, float &v) { v = j < i ? -v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
-            each(xp, m0, nC, [&](int i, int j, float &v) { v = j <= i ? v * ex2_mufu(cs[i] - cs[j]) : 0.f; });
+#pragma unroll
+            for (int m = 0; m < 2; m++)
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int i = m0 + 16 * m + gq + 8 * (e >> 1), j = nC + 8 * q + 2 * tq + (e & 1);
+                        const float G = gdr_between(cs[i], cl[i], cs[j], cl[j]);
+                        xa[m][q][e] = j < i ? -xa[m][q][e] * G : 0.f;
+                        xp[m][q][e] = j <= i ? xp[m][q][e] * G : 0.f;
+                    }
             float kk[2][2][4], qk[2][2][4];
             zero(kk);
             zero(qk);
@@ -948,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
             __syncthreads();
             fetch(i + 2);
         }
-        each(Y, m0, nK, [&](int i, int, float &v) { v *= ex2_mufu(end - cs[i]); });
+        each(Y, m0, nK, [&](int i, int, float &v) { v *= gdr_between(end, endl, cs[i], cl[i]); });
         {
             float kz[4] = {};
             dots(Y, m0, nK, Kt, kz);

@@ -79,7 +79,8 @@ constexpr int kOffP = kOffV + 2 * 2 * kTile;
 constexpr int kOffT = kOffP + kP * 2 * kTile;
 constexpr int kOffVec = kOffT + 2 * 2 * kTile;
 struct Vec {               // of one chunk
-    float ncs[kC], rk[kC]; // -cs, 1 / |k| (apart: neighbours make pairs for packed arithmetic)
+    float ncs[kC], ncl[kC]; // -cs as hi + lo
+    float rk[kC];          // 2^-lo / |k| (each array apart: neighbours make pairs for packed arithmetic)
     float4 bg[kC / 2];     // b of two steps, their -b c / |k|
     float gq[kC];          // c scale / |q| (first 1 / |q|)
     float ek[kC];          // e / |k|
@@ -378,12 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int m = 0; m < 2; m++) {
                         float *n = m ? ve->gq : ve->rk;
-                        n[r0] = rsqrtf(((lane >> 2) & 1 ? acc[m][0][1] : acc[m][0][0]) + kL2Eps);
-                        n[r0 + 8] = rsqrtf(((lane >> 2) & 1 ? acc[m][1][3] : acc[m][1][2]) + kL2Eps);
+                        const float w = m ? 0.f : 1.f;
+                        n[r0] = rsqrtf(((lane >> 2) & 1 ? acc[m][0][1] : acc[m][0][0]) + kL2Eps) * gdr_rest(w, ve->ncl[r0]);
+                        n[r0 + 8] =
+                            rsqrtf(((lane >> 2) & 1 ? acc[m][1][3] : acc[m][1][2]) + kL2Eps) * gdr_rest(w, ve->ncl[r0 + 8]);
                     }
                 }
             } else if (!isq) {
-                ve->rk[i] = 1.f;
+                ve->rk[i] = gdr_rest(1.f, ve->ncl[i]);
             } else {
                 ve->gq[i] = 1.f;
             }
@@ -391,7 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(&bars.team[team][0], turn & 1) || !wait(&bars.kk[team], turn & 1))
                 break;
             fence_after();
-            const float csi = -ve->ncs[i], f = isq ? a.scale * ve->gq[i] : ve->rk[i] * ve->b[i];   // the row's factor
+            // the row's factor, 2^lo in it; a column's, rk, has 2^-lo
+            const float csi = -ve->ncs[i], nl = ve->ncl[i];
+            const float f = isq ? a.scale * ve->gq[i] * gdr_rest(-1.f, nl) : ve->rk[i] * ve->b[i] * gdr_rest(-2.f, nl);
             const int last = isq ? i : i - 1, blk = i >> 4, il = i & 15;
             // rows of 16 as bf16 pairs: of P; of A left of the diagonal block, that block's inverse in it
             auto put = [&](uint8_t *to, int at_blk, const float (&x)[16]) {
@@ -515,15 +520,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             if (pw == 0) {   // no blocks left of the first: the scalars instead
-                const float end = -ve->ncs[kC - 1];
+                const float end = -ve->ncs[kC - 1], rest = gdr_rest(-1.f, ve->ncl[kC - 1]);
 #pragma unroll
                 for (int s = 0; s < 2; s++) {
                     const int at = lane + 32 * s;
                     const float nc = ve->ncs[at], rk = ve->rk[at], bb = ve->b[at];
                     float *bg = reinterpret_cast<float *>(&ve->bg[at / 2]) + (at & 1);
                     bg[0] = bb;
-                    bg[2] = -bb * ex2_mufu(-nc) * rk;
-                    ve->ek[at] = ex2_mufu(end + nc) * rk;
+                    bg[2] = -bb * ex2_mufu(-nc) * rk * gdr_rest(-2.f, ve->ncl[at]);
+                    ve->ek[at] = ex2_mufu(end + nc) * rest * rk;
                 }
                 if (lane == 0)
                     ve->dec = ex2_mufu(end);
@@ -711,13 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bb[e] = in ? (a.sigmoid ? gdr_sigmoid(be[e]) : be[e]) : 0.f;
             }
             fetch(c + 1);
-            float incl = g[0] + g[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float u = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += u;
-            }
+            float2 cs[2];
+            gdr_log_sums(g, cs);
             if (c >= kKQ && !wait(&bars.empty[c % kKQ], phase(c - kKQ)))
                 break;
             if (__any_sync(0xffffffffu, *abort))
@@ -742,8 +742,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             issued = c;
             Vec *ve = vec(c);
-            ve->ncs[2 * lane] = g[1] - incl;
-            ve->ncs[2 * lane + 1] = -incl;
+            *reinterpret_cast<float2 *>(&ve->ncs[2 * lane]) = make_float2(-cs[0].x, -cs[1].x);
+            *reinterpret_cast<float2 *>(&ve->ncl[2 * lane]) = make_float2(-cs[0].y, -cs[1].y);
             ve->b[2 * lane] = bb[0];
             ve->b[2 * lane + 1] = bb[1];
             bar_arrive(&bars.scal[c % kVecs]);

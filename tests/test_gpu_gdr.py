@@ -323,3 +323,16 @@ def test_python_refusals(cuda_device):
         ssm.gdr_chunk_fwd(wide, wide, *args[2:])
     with pytest.raises((ValueError, TypeError)):
         ssm.gdr_chunk_fwd(*args, initial_state=torch.zeros(1, 1, 64, 64, device="cuda", dtype=BF16))
+
+
+@pytest.mark.parametrize("every", [4, 8, 23])
+def test_many_short_packed_sequences(cuda_device, every):
+    """A step that forgets everything every few steps: log decays that have reached thousands leave the
+    decays between neighbours their low bits, and the tolerances stay as they are."""
+    x = make(1, 200, 1, 2, 128, 128, seed=every, init=True)
+    x["delta"][:, every::every] = 1e4
+    out, last = run_fwd(x, {})
+    ro, rs = ob.gdr(**f64(x))
+    close(out, ro, False)
+    close(last, rs, True)
+    check_bwd(x, {})
