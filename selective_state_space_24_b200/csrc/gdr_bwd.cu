@@ -144,11 +144,14 @@ template <class F> __device__ __forceinline__ Scaled<F> scaled(F f, const float 
 
 __device__ __forceinline__ float bf(const bf16 *p) { return __bfloat162float(*p); }
 
-// tf32 keeps the upper 19 bits of a float32: cut off, or rounded.  (Integer
-// operations: the conversion instruction runs on the slow pipe and bounded
-// the products.)
-__device__ __forceinline__ uint32_t tf32_cut(float x) { return __float_as_uint(x) & 0xffffe000u; }
-__device__ __forceinline__ uint32_t tf32_round(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
+// tf32 keeps the upper 19 bits of a float32, and the product cuts off the
+// rest.  The first part is rounded, so that the second has either sign and its
+// cutting no bias (both cut, every operand is a little small, and dA and
+// ddelta_bias are 1e-6 off instead of 4e-7; rounding the second part too
+// changes nothing).  (Integer operations: the conversion instruction runs on
+// the slow pipe and bounded the products.)  tf32_up leaves what will be cut.
+__device__ __forceinline__ uint32_t tf32_up(float x) { return __float_as_uint(x) + 0x1000u; }
+__device__ __forceinline__ uint32_t tf32_round(float x) { return tf32_up(x) & 0xffffe000u; }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
 {
     asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -164,7 +167,7 @@ template <Part P, int N> __device__ __forceinline__ void parts(const float (&x)[
 {
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        hi[i] = P == kExact ? __float_as_uint(x[i]) : P == kOne ? tf32_round(x[i]) : tf32_cut(x[i]);
+        hi[i] = P == kExact ? __float_as_uint(x[i]) : P == kOne ? tf32_up(x[i]) : tf32_round(x[i]);
         lo[i] = P == kTwo ? __float_as_uint(x[i] - __uint_as_float(hi[i])) : 0u;
     }
 }

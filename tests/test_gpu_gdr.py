@@ -336,3 +336,20 @@ def test_many_short_packed_sequences(cuda_device, every):
     close(out, ro, False)
     close(last, rs, True)
     check_bwd(x, {})
+
+
+@pytest.mark.parametrize("size", [(1, 320, 4, 8, 128, 128), (2, 200, 8, 8, 64, 64)], ids=str)
+def test_sums_over_steps_keep_float32(cuda_device, size):
+    """dA and ddelta_bias to 1e-6 in the 2-norm.  Two tf32 parts, the first rounded, leave at most 2^-11 and then
+    2^-22 of the value, about 2^-24 in the mean square; the product of two second parts, which is left out, is
+    2^-22 at most and as much in the mean.  With float32's own additions some 1.5e-7 a product,
+    without a sign of its own, and ten products in a row from the inputs to these sums: 5e-7; twice that is asked."""
+    x = make(*size, seed=21, init=True)
+    gen = torch.Generator().manual_seed(3)
+    dout = torch.randn(x["v"].shape, generator=gen).to(BF16)
+    g = run_bwd(x, dout)
+    t = f64(x, grad=True)
+    out, _ = ob.gdr(**t)
+    for n, w in zip(("dA", "ddelta_bias"), torch.autograd.grad((out * dout.double()).sum(), [t["A"], t["delta_bias"]])):
+        far = float((g[n].double().cpu() - w).norm() / w.norm())
+        assert far <= 1e-6, (n, far)
