@@ -162,6 +162,7 @@ ssm::ResidualArgs residual_args(const norm_dims *d, const residual_norm_params *
     a.rows = d->rows;
     a.samples = p->samples;
     a.dim = (int)d->dim;
+    a.fdim = (float)d->dim;
     a.eps = d->eps;
     a.alpha = p->alpha;
     a.dtype = d->dtype == SSM_F32 ? 0 : 1;

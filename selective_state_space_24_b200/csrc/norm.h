@@ -36,6 +36,7 @@ struct ResidualArgs {
     int64_t rows, samples;
     int dim;
     float eps, alpha;
+    float fdim;                // dim (read as a constant, it takes no register: 9 blocks per SM, not 8)
     int dtype, layer, res32;   // res32: the stream is float32
     const void *x, *residual, *dout, *dres_out;
     const float *weight, *bias, *scale, *post;

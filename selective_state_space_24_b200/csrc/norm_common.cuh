@@ -120,7 +120,7 @@ template <int N> __device__ __forceinline__ void load_f32(const float *p, float 
         f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
     }
 }
-constexpr int kRedMax = 4;   // values summed at once
+constexpr int kRedMax = 3;   // values summed at once
 // shared memory of row_sum: two buffers in turn, so that one barrier per sum
 // is enough (a buffer is written again only after the next sum's barrier)
 struct __align__(16) RedSmem {
@@ -156,6 +156,15 @@ template <int K, int M> __device__ __forceinline__ void row_sum(float (&v)[M], i
         }
         turn ^= 1;
     }
+}
+
+// The mean from a sum over n values: the rounded product's remainder, exact in
+// one fma, is divided too.  So a row of one value c has the mean c wherever n c
+// is a float32.
+__device__ __forceinline__ float mean_of(float sum, float n, float inv)
+{
+    const float q = sum * inv;
+    return fmaf(fmaf(-n, q, sum), inv, q);
 }
 
 // the sum over a warp's lanes

@@ -10,8 +10,8 @@
 //     dpost = sum dt x p, e = dt post,  dx = p (e - x p mean(e x p))   (dx = dt without post)
 //     dweight = sum dout y, dbias = sum dout
 //
-// Bound by HBM: one pass, a row stays in registers through up to three
-// dependent sums (the mean is taken before the squares, which keeps the
+// Bound by HBM: one pass, a row stays in registers through up to four
+// dependent sums (the mean is taken off before the squares, which keeps the
 // variance exact for rows far from zero).  Thread layout and column sums as
 // in gated_norm.cu; with a scale per sample a block's rows are of one sample.
 // residual_out is rounded once to its type and the norm reads that value, so
@@ -39,50 +39,43 @@ int64_t parts_for(int64_t rows, int64_t sets, const NormPlan &p, int64_t most)
 // gradient is summed over each of them, else all rows are one.
 int64_t row_sets(int64_t samples, bool has_scale) { return has_scale ? samples : 1; }
 
-// a row's mean (LAYER) and (mean square + eps)^-1/2 from its registers; r is
-// centred in place.  The rounded mean of a row far from zero is off by up to
-// half a step of that mean; the centred values (exact differences) show by
-// how much, in the same sum that takes their squares.
+// A row's (mean square + eps)^-1/2 from its registers, with LAYER after the
+// mean is taken off in place.  The float32 mean of a row far from zero is off
+// by some steps of that mean; the sum of the centred values (exact differences,
+// so the product is rounded before it is taken off) shows by how much, and the
+// squares are summed when that is off too.  Both in one sum, off^2 taken off the
+// mean square afterwards, saves 1 us of 14.5 (12608 rows of 384), but leaves
+// rows that vary by less than that error, or not at all, a variance of rounding
+// errors, which may be negative.
 template <bool LAYER, int NV, int E>
-__device__ __forceinline__ float norm_stats(float (&r)[NV][E], const bool (&in)[NV], float inv, float eps, int tpr,
-                                            RedSmem &red, int &turn)
+__device__ __forceinline__ float norm_stats(float (&r)[NV][E], const bool (&in)[NV], float n, float inv, float eps,
+                                            int tpr, RedSmem &red, int &turn)
 {
-    float s[2] = {0.f, 0.f};
-    if (LAYER) {
-        float m[1] = {0.f};
+    if (LAYER)
 #pragma unroll
-        for (int v = 0; v < NV; v++)
+        for (int pass = 0; pass < 2; pass++) {   // the mean, then what its rounding left
+            float m[1] = {0.f};
 #pragma unroll
-            for (int e = 0; e < E; e++)
-                m[0] += r[v][e];   // zero outside the row
-        row_sum<1>(m, tpr, red, turn);
-        m[0] *= inv;
+            for (int v = 0; v < NV; v++)
 #pragma unroll
-        for (int v = 0; v < NV; v++)
+                for (int e = 0; e < E; e++)
+                    m[0] += r[v][e];   // zero outside the row
+            row_sum<1>(m, tpr, red, turn);
+            m[0] = pass == 0 ? __fmul_rn(m[0], inv) : mean_of(m[0], n, inv);
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                r[v][e] = in[v] ? r[v][e] - m[0] : 0.f;
-                s[1] += r[v][e];
-            }
-    }
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    r[v][e] = in[v] ? r[v][e] - m[0] : 0.f;
+        }
+    float s[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < NV; v++)
 #pragma unroll
         for (int e = 0; e < E; e++)
             s[0] = fmaf(r[v][e], r[v][e], s[0]);
-    if (LAYER) {
-        row_sum<2>(s, tpr, red, turn);
-        const float off = s[1] * inv;
-#pragma unroll
-        for (int v = 0; v < NV; v++)
-#pragma unroll
-            for (int e = 0; e < E; e++)
-                r[v][e] -= in[v] ? off : 0.f;
-        return rsqrtf(fmaf(-off, off, s[0] * inv) + eps);
-    }
-    float one[1] = {s[0]};
-    row_sum<1>(one, tpr, red, turn);
-    return rsqrtf(one[0] * inv + eps);
+    row_sum<1>(s, tpr, red, turn);
+    return rsqrtf(s[0] * inv + eps);
 }
 
 template <typename R> __device__ __forceinline__ float rounded(float v);
@@ -162,7 +155,7 @@ __global__ void __launch_bounds__(512) residual_fwd_kernel(const ResidualArgs a,
             if (live && in[v])
                 store_row<R, E>(static_cast<R *>(a.res_out) + row * a.dim + (lane_r + v * tpr) * E, rv[v]);
         }
-        const float k = norm_stats<LAYER>(rv, in, inv, a.eps, tpr, red, turn);
+        const float k = norm_stats<LAYER>(rv, in, a.fdim, inv, a.eps, tpr, red, turn);
 #pragma unroll
         for (int v = 0; v < NV; v++)
             if (live && in[v]) {
@@ -245,31 +238,9 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
             xr.get(t);
         if (r0 + stride < row_end)
             fetch(r0 + stride);
-        // the sums that need nothing else go together: of r^2 (of r, then of
-        // its centred squares), of g r, g and x^2
-        float sx = 0.f;
-        if (POST)
-#pragma unroll
-            for (int v = 0; v < NV; v++)
-#pragma unroll
-                for (int e = 0; e < E; e++)
-                    sx = fmaf(t[v][e], t[v][e], sx);
-        if (LAYER) {
-            float m[2] = {0.f, sx};
-#pragma unroll
-            for (int v = 0; v < NV; v++)
-#pragma unroll
-                for (int e = 0; e < E; e++)
-                    m[0] += y[v][e];
-            row_sum<2>(m, tpr, red, turn);
-            sx = m[1];
-#pragma unroll
-            for (int v = 0; v < NV; v++)
-#pragma unroll
-                for (int e = 0; e < E; e++)
-                    y[v][e] = in[v] ? y[v][e] - m[0] * inv : 0.f;
-        }
-        float s[4] = {0.f, 0.f, LAYER ? 0.f : sx, 0.f};
+        // the sums that need nothing else go together: of r^2, g r and x^2; for
+        // the layer norm of r, g and x^2, then of what the mean left of r (as in
+        // norm_stats), then of r^2 and g r
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             gc.get(v, g[v]);
@@ -280,23 +251,58 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
             if (in[v])
                 load_f32<E>(a.weight + (lane_r + v * tpr) * E, w);
 #pragma unroll
-            for (int e = 0; e < E; e++) {
+            for (int e = 0; e < E; e++)
                 g[v][e] *= w[e];
+        }
+        float sx = 0.f, mg = 0.f;
+        if (POST)
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    sx = fmaf(t[v][e], t[v][e], sx);
+        if (LAYER) {
+            float m[3] = {0.f, 0.f, sx}, off[1] = {0.f};
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    m[0] += y[v][e];
+                    m[1] += g[v][e];
+                }
+            row_sum<3>(m, tpr, red, turn);
+            const float mean = __fmul_rn(m[0], inv);
+            mg = m[1] * inv;
+            sx = m[2];
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    y[v][e] = in[v] ? y[v][e] - mean : 0.f;
+                    off[0] += y[v][e];
+                }
+            row_sum<1>(off, tpr, red, turn);
+            off[0] = mean_of(off[0], a.fdim, inv);
+#pragma unroll
+            for (int v = 0; v < NV; v++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    y[v][e] -= in[v] ? off[0] : 0.f;
+        }
+        float s[3] = {0.f, 0.f, sx};
+#pragma unroll
+        for (int v = 0; v < NV; v++)
+#pragma unroll
+            for (int e = 0; e < E; e++) {
                 s[0] = fmaf(y[v][e], y[v][e], s[0]);
                 s[1] = fmaf(g[v][e], y[v][e], s[1]);
-                if (LAYER) {
-                    s[2] += y[v][e];   // the rounded mean's error, as in norm_stats
-                    s[3] += g[v][e];
-                }
             }
-        }
-        row_sum<LAYER ? 4 : 3>(s, tpr, red, turn);
+        row_sum<LAYER ? 2 : 3>(s, tpr, red, turn);
         if (!LAYER)
             sx = s[2];
-        const float off = LAYER ? s[2] * inv : 0.f, mg = LAYER ? s[3] * inv : 0.f;
         // behind the last row 0, so that eps = 0 leaves no 0 / 0 in dweight
-        const float k = live ? rsqrtf(fmaf(-off, off, s[0] * inv) + a.eps) : 0.f;
-        const float mgy = k * (s[1] * inv - off * mg);   // mean(g y)
+        const float k = live ? rsqrtf(s[0] * inv + a.eps) : 0.f;
+        const float mgy = k * (s[1] * inv);   // mean(g y)
 #pragma unroll
         for (int v = 0; v < NV; v++)
             if (in[v]) {
@@ -304,7 +310,7 @@ __global__ void __launch_bounds__(512) residual_bwd_kernel(const ResidualArgs a,
                 gc.get(v, o);
 #pragma unroll
                 for (int e = 0; e < E; e++) {
-                    y[v][e] = (y[v][e] - off) * k;
+                    y[v][e] *= k;
                     dw[v][e] = fmaf(o[e], y[v][e], dw[v][e]);
                     if (BIAS)
                         db[v][e] += o[e];

@@ -211,3 +211,44 @@ def test_python_refusals(cuda_device):
         ssm.residual_norm_fwd(x, w, scale=torch.ones(3, 64, device="cuda"))
     with pytest.raises((ValueError, TypeError)):
         ssm.residual_norm_fwd(x, w, residual=x.to(BF16))
+
+
+@pytest.mark.parametrize("dim", [8, 200, 384, 1000, 5000, 8192])
+@pytest.mark.parametrize("eps", [1e-5, 1e-12])
+def test_layer_norm_of_constant_rows(cuda_device, dim, eps):
+    """A row of one value, however large, is zero after its mean is taken off: bias is left, finite gradients,
+    and nothing in the sums over rows that the other rows did not put there."""
+    gen = torch.Generator().manual_seed(dim)
+    value = torch.tensor([0.0, 3.0, -0.1, 1e3, 12345.678, 1.7e6, -2.24e8, 2.24e8, 1.23e9, 7.7e12, -3.3e17, 2.0])
+    x = value[:, None].expand(-1, dim).contiguous()
+    x[-1] = r(gen, dim)
+    w, b, dy = r(gen, dim).abs() + 0.5, r(gen, dim), r(gen, len(value), dim)
+    y, ro = ssm.residual_norm_fwd(x.cuda(), w.cuda(), bias=b.cuda(), layer_norm=True, eps=eps)
+    assert torch.equal(ro.cpu(), x) and bool((y[:-1] == b.cuda()).all())
+    s, ws = ob.f64(x, True), ob.f64(w, True)
+    o = ob.norm(s, ws, bias=ob.f64(b), layer_norm=True, eps=eps)
+    close(y, o)
+    g = ssm.residual_norm_bwd(x.cuda(), ro, w.cuda(), dy.cuda(), bias=b.cuda(), layer_norm=True, eps=eps)
+    assert all(bool(torch.isfinite(t).all()) for t in g.values())
+    only = ssm.residual_norm_bwd(x[-1:].cuda(), ro[-1:].contiguous(), w.cuda(), dy[-1:].cuda(), bias=b.cuda(), layer_norm=True,
+                                 eps=eps)
+    assert torch.equal(g["dweight"], only["dweight"])
+    dx, _ = torch.autograd.grad(o, [s, ws], dy.double())
+    for k in range(len(value)):
+        close(g["dx"][k], dx[k])
+
+
+def test_layer_norm_of_nearly_constant_rows(cuda_device):
+    """Rows that vary by a few steps of their values: the variance is that of the values, not of the mean's rounding."""
+    gen = torch.Generator().manual_seed(9)
+    for dim in (200, 1000, 5000):
+        x = 2.24e8 + 16.0 * torch.randint(-3, 4, (20, dim), generator=gen)
+        w, dy = r(gen, dim).abs() + 0.5, r(gen, 20, dim)
+        y, ro = ssm.residual_norm_fwd(x.cuda(), w.cuda(), layer_norm=True)
+        s, ws = ob.f64(ro, True), ob.f64(w, True)
+        o = ob.norm(s, ws, layer_norm=True)
+        close(y, o)
+        g = ssm.residual_norm_bwd(x.cuda(), ro, w.cuda(), dy.cuda(), layer_norm=True)
+        dx, dw = torch.autograd.grad(o, [s, ws], dy.double())
+        close(g["dx"], dx)
+        close(g["dweight"], dw, True)
