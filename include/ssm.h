@@ -523,8 +523,8 @@ SSM_API size_t gdr_chunk_workspace_size(const gdr_dims *dims);
  *                 last_state (updated in place)
  *   last_state    (B, Hv, V, K) float32 or NULL: the state after the last step
  * A padded position with dt = 0 and b = 0 (and finite q, k, v) leaves the
- * state as it is; a position with a large dt (dt A below -104) forgets it, so
- * several sequences can be packed into one.  An empty call (B, L, Hk or Hv
+ * state as it is; a position with a large dt (dt A below -104, an infinite dt
+ * too) forgets it, so several sequences can be packed into one.  An empty call (B, L, Hk or Hv
  * zero) launches no kernel and copies initial_state (or zeros) to last_state.
  * A NaN or infinity in a row of q, k or v makes its head's outputs undefined
  * from the start of the row's chunk on: fill the padding.
@@ -563,8 +563,10 @@ SSM_API size_t gdr_chunk_bwd_workspace_size(const gdr_dims *dims);
  * or NULL).  The states are recomputed, so nothing from the forward call is
  * needed (but a workspace of about 4 KB per step and value head, K = V = 128).
  * Every gradient is written, not accumulated, and summed in a fixed order: the
- * same call gives the same bits.  initial_state NULL means zero.  An empty
- * call writes zeros, and dlast_state to dinitial_state.
+ * same call gives the same bits.  initial_state NULL means zero.  A position
+ * that forgets everything has no gradient through its dt.  An empty call writes
+ * zeros, and dlast_state to dinitial_state.  As forward, NaN and infinities in
+ * the padding (q, k, v, dout) spread: fill it.
  */
 SSM_API ssm_status gdr_chunk_bwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state,
                                  const void *dout, const float *dlast_state, const gdr_grads *grads,

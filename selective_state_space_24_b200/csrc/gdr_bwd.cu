@@ -1017,7 +1017,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
                 if (row < valid) {
                     const size_t at = (tok + row) * a.Hv + h;
                     const float pre = s.delta[row];
-                    sA = fmaf(dg[i], gdr_dt(pre, bias, a.softplus), sA);
+                    // a step that leaves nothing has no gradient, not 0 times an infinite dt either
+                    sA = dg[i] != 0.f ? fmaf(dg[i], gdr_dt(pre, bias, a.softplus), sA) : sA;
                     const float dd = dg[i] * Ah * (a.softplus ? gdr_sigmoid(pre + bias) : 1.f);
                     sb += dd;
                     gdr_st(static_cast<bf16 *>(ga.ddelta), at, dd);

@@ -353,3 +353,21 @@ def test_sums_over_steps_keep_float32(cuda_device, size):
     for n, w in zip(("dA", "ddelta_bias"), torch.autograd.grad((out * dout.double()).sum(), [t["A"], t["delta_bias"]])):
         far = float((g[n].double().cpu() - w).norm() / w.norm())
         assert far <= 1e-6, (n, far)
+
+
+@pytest.mark.parametrize("softplus", [True, False])
+def test_infinite_step_between_packed_sequences(cuda_device, softplus):
+    """delta = inf forgets like any other step that leaves nothing: the bits of 1e4, in the sums over steps too."""
+    x = make(1, 150, 1, 2, 128, 64, seed=12, init=True)
+    x["delta"] = x["delta"].abs()
+    if not softplus:   # dt = delta, not negative
+        x["delta_bias"] = None
+    flags = dict(delta_softplus=softplus)
+    dout = torch.randn(x["v"].shape, generator=torch.Generator().manual_seed(2)).to(BF16)
+    got = []
+    for step in (1e4, float("inf")):
+        x["delta"][:, [70, 101]] = step
+        got.append(run_bwd(x, dout, flags=flags) | dict(zip(("out", "last"), run_fwd(x, flags))))
+    for n in got[0]:
+        assert torch.isfinite(got[1][n]).all(), n
+        assert torch.equal(got[0][n], got[1][n]), n
