@@ -692,6 +692,11 @@ SSM_API ssm_status ssm_check_device(void *stream);
  */
 SSM_API void ssm_debug_ssd_stall(int withhold_chunk, unsigned wait_limit);
 
+/* The same for the chunked kernel of gdr_chunk_fwd (whose short sequences go
+ * step by step and have no waits): the warp that brings a chunk's gates never
+ * signals those of `withhold_chunk`.  last_state is then not written. */
+SSM_API void ssm_debug_gdr_stall(int withhold_chunk, unsigned wait_limit);
+
 /*
  * Test hook for the choice between the thread layouts of the plain S6 scans
  * (ssm_scan_fwd, ssm_scan_fwd_state, ssm_scan_fwd_noalloc, bidir_scan_fwd and

@@ -89,6 +89,7 @@ _int = ctypes.c_int
 # exported name -> (restype, argtypes)
 SIGNATURES = {
     "ssm_debug_ssd_stall": (None, [_int, ctypes.c_uint]),
+    "ssm_debug_gdr_stall": (None, [_int, ctypes.c_uint]),
     "ssm_debug_s6_mapping": (_int, [_int]),
     "ssm_scan_workspace_size": (_sz, [ctypes.POINTER(ssm_dims)]),
     "ssm_scan_fwd": (_int, [ctypes.POINTER(ssm_dims), _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp,

@@ -19,6 +19,8 @@ struct GdrArgs {
     void *out;
     float *last;                     // (B, Hv, V, K) or nullptr
     void *workspace;
+    unsigned wait_limit;             // gdr_stall_set's, of a call that is to stall
+    int withhold_chunk;
 };
 
 // Step by step, the state in registers: one token (gdr_step) or short
@@ -27,6 +29,9 @@ cudaError_t launch_gdr_recurrent(const GdrArgs &a, cudaStream_t st);
 
 size_t gdr_chunk_ws_bytes(const GdrArgs &a);
 cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st);
+// Test setting of the chunked forward kernel's bounded waits (process-wide):
+// the chunk to withhold (< 0: none) and the waits' limit (0: the default).
+void gdr_stall_set(int withhold_chunk, unsigned wait_limit);
 // The kernels' device-side error word (a bounded wait that gave up).
 cudaError_t read_and_clear_gdr_error(unsigned *value, cudaStream_t stream);
 

@@ -53,6 +53,7 @@
 // 4.70 -> 4.15.  (One code for all rows of T saves another 4 KB, 148 blocks
 // 3.80 us, but lengthens T's latency: 128 blocks 3.95; loops of single products
 // issue too slowly: 16 blocks 3.47 -> 3.65.)
+#include <atomic>
 #include <type_traits>
 
 #include "gdr_math.cuh"
@@ -115,7 +116,9 @@ constexpr int kStateWarps = 16, kTeamWarp = 16, kMmaWarp = 24, kLoadWarp = 25, k
 // up 32 x 128, the two teams take 16 x 256.
 constexpr int kRegsTeam = 88, kRegsIssue = 40;
 
-template <int K>
+// STALL: the same kernel for the test of its waits' end, with their limit and a
+// chunk to withhold from the arguments (read in every call, they cost 11%).
+template <int K, bool STALL>
 __global__ void __launch_bounds__(kThreads, 1)
     gdr_chunk_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                      const __grid_constant__ CUtensorMap mapV, const __grid_constant__ CUtensorMap mapO, const GdrArgs a, const int nch)
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort = &bars.abort;
     bool failed = false;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (warp_wait(bar, parity, abort))
+        if (warp_wait(bar, parity, abort, STALL ? a.wait_limit : kWaitLimit))
             return true;
         failed = true;
         return false;
@@ -746,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<float2 *>(&ve->ncl[2 * lane]) = make_float2(-cs[0].y, -cs[1].y);
             ve->b[2 * lane] = bb[0];
             ve->b[2 * lane + 1] = bb[1];
-            bar_arrive(&bars.scal[c % kVecs]);
+            if (!STALL || c != a.withhold_chunk)
+                bar_arrive(&bars.scal[c % kVecs]);
         }
         if (lane == 0)
             for (int c = max(0, issued - kKQ + 1); c <= issued; c++)
@@ -790,20 +794,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_free(tm, kTmemCols);
 }
 
-template <int K> cudaError_t launch(const GdrArgs &a, cudaStream_t st)
+template <int K, bool STALL> cudaError_t launch(const GdrArgs &a, cudaStream_t st)
 {
     CUtensorMap q, k, v, o;
     if (!tc::head_map(&q, a.q, a.Bsz, a.L, a.Hk, a.K, true) || !tc::head_map(&k, a.k, a.Bsz, a.L, a.Hk, a.K, true) ||
         !tc::head_map(&v, a.v, a.Bsz, a.L, a.Hv, a.V, false) || !tc::head_map(&o, a.out, a.Bsz, a.L, a.Hv, a.V, false))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(gdr_chunk_kernel<K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(gdr_chunk_kernel<K, STALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess)
         return e;
-    gdr_chunk_kernel<K><<<(unsigned)((int64_t)a.Bsz * a.Hv), kThreads, kSmem, st>>>(q, k, v, o, a, (a.L + kC - 1) / kC);
+    gdr_chunk_kernel<K, STALL><<<(unsigned)((int64_t)a.Bsz * a.Hv), kThreads, kSmem, st>>>(q, k, v, o, a, (a.L + kC - 1) / kC);
     return cudaGetLastError();
 }
 
 }  // namespace
+
+static std::atomic<int> g_withhold_chunk{-1};
+static std::atomic<unsigned> g_wait_limit{0};
+
+void gdr_stall_set(int withhold_chunk, unsigned wait_limit)
+{
+    g_withhold_chunk.store(withhold_chunk);
+    g_wait_limit.store(wait_limit);
+}
 
 size_t gdr_chunk_ws_bytes(const GdrArgs &) { return 0; }
 
@@ -829,7 +842,15 @@ cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st)
 {
     if (a.L <= recurrent_limit(a))
         return launch_gdr_recurrent(a, st);
-    return a.K == 128 ? launch<128>(a, st) : launch<64>(a, st);
+    const unsigned limit = g_wait_limit.load();
+    const int chunk = g_withhold_chunk.load();
+    if (limit || chunk >= 0) {
+        GdrArgs b = a;
+        b.wait_limit = limit ? limit : tc::kWaitLimit;
+        b.withhold_chunk = chunk;
+        return a.K == 128 ? launch<128, true>(b, st) : launch<64, true>(b, st);
+    }
+    return a.K == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
 }
 
 cudaError_t read_and_clear_gdr_error(unsigned *value, cudaStream_t stream)

@@ -747,6 +747,8 @@ ssm_status ssm_check_device(void *stream)
 
 void ssm_debug_ssd_stall(int withhold_chunk, unsigned wait_limit) { ssm::ssd_stall_set(withhold_chunk, wait_limit); }
 
+void ssm_debug_gdr_stall(int withhold_chunk, unsigned wait_limit) { ssm::gdr_stall_set(withhold_chunk, wait_limit); }
+
 ssm_status ssm_debug_s6_mapping(int mode)
 {
     if (mode < 0 || mode > 3)

@@ -41,18 +41,18 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
 }
 __device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity) { return bar_test(smem_u32(bar), parity); }
 
-constexpr int kWaitLimit = 1 << 20;    // polls of a pipeline wait
+constexpr unsigned kWaitLimit = 1u << 20;   // polls of a pipeline wait, unless a test asks for fewer
 constexpr int kDrainLimit = 1 << 22;   // polls of a wait for this block's own copies and products
 
-// Bounded wait of a whole warp.  False: it gave up, or found the block's abort
+// Bounded wait of a whole warp.  False: it gave up after `limit` polls, or found the block's abort
 // word set.  The caller then leaves its loop and calls gave_up, and every later
 // wait of the block gives up at once: the kernel ends promptly, with wrong
 // values, and says so.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned limit)
 {
     const uint32_t b = smem_u32(bar);
 #pragma unroll 1
-    for (int it = 0; it < kWaitLimit; it++) {   // each test waits a while by itself
+    for (unsigned it = 0; it < limit; it++) {   // each test waits a while by itself
         if (__all_sync(0xffffffffu, bar_test(b, parity)))
             return true;
         if (__any_sync(0xffffffffu, *abort))

@@ -371,3 +371,28 @@ def test_infinite_step_between_packed_sequences(cuda_device, softplus):
     for n in got[0]:
         assert torch.isfinite(got[1][n]).all(), n
         assert torch.equal(got[0][n], got[1][n]), n
+
+
+@pytest.mark.parametrize("K", [64, 128])
+@pytest.mark.parametrize("chunk", [0, 2, 4])
+def test_device_timeout_is_reported_and_the_next_call_is_clean(cuda_device, K, chunk):
+    """A bounded wait that runs out: the gates of one chunk are never signalled (nothing else gives that signal),
+    and every wait ends after 4096 polls.  The call completes: it waits for the copies and products that it issued
+    and frees its tensor memory.  ssm_check_device reports it once, and the next call gives the bits of the one before."""
+    lib = ssm.capi()
+    x = make(2, 320, 1, 3, K, 128, seed=31, init=True)
+    want = run_fwd(x, {})
+    c = cuda(x)
+    args = [c.pop(n) for n in ("q", "k", "v", "delta", "A", "beta")]
+    last = torch.full((2, 3, 128, K), 7.0, device="cuda")
+    lib.ssm_debug_gdr_stall(chunk, 1 << 12)
+    try:
+        ssm.gdr_chunk_fwd(*args, last_state=last, **c)
+        status = lib.ssm_check_device(torch.cuda.current_stream().cuda_stream)
+    finally:
+        lib.ssm_debug_gdr_stall(-1, 0)
+    assert status == 7, ssm.STATUS.get(status, status)
+    assert lib.ssm_check_device(torch.cuda.current_stream().cuda_stream) == 0   # cleared
+    assert bool((last == 7.0).all())
+    out, again = run_fwd(x, {})
+    assert torch.equal(out, want[0]) and torch.equal(again, want[1])
