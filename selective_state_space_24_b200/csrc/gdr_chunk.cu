@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float nc = ve->ncs[at], rk = ve->rk[at], bb = ve->b[at];
                     float *bg = reinterpret_cast<float *>(&ve->bg[at / 2]) + (at & 1);
                     bg[0] = bb;
-                    bg[2] = -bb * ex2_mufu(-nc) * rk * gdr_rest(-2.f, ve->ncl[at]);
+                    bg[2] = -bb * ex2_mufu(-nc) * rk;   // c to 2^-24 |cs| (lo, and rk's), as it is 2^cs
                     ve->ek[at] = ex2_mufu(end + nc) * rest * rk;
                 }
                 if (lane == 0)

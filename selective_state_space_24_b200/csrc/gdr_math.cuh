@@ -52,8 +52,8 @@ __device__ __forceinline__ void gdr_log_sums(const float (&g)[2], float2 (&cs)[2
     auto from_below = [&](int o) {
         return make_float2(__shfl_up_sync(0xffffffffu, incl.x, o), __shfl_up_sync(0xffffffffu, incl.y, o));
     };
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {   // (small code: see gdr_chunk.cu)
         const float2 u = from_below(o);
         if (lane >= o)
             incl = pair_add(u, incl);
