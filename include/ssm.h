@@ -503,8 +503,9 @@ typedef struct {
     int32_t qk_l2norm;        /* 1: q and k are divided by sqrt(sum of squares + 1e-6)  */
 } gdr_inputs;
 
-/* Bytes of device workspace gdr_chunk_fwd needs for `dims` (0 if none or if
- * dims are not supported). */
+/* Bytes of device workspace gdr_chunk_fwd needs: 0, its states and tiles stay
+ * on the SMs.  The call takes a workspace like its siblings and does not look
+ * at it. */
 SSM_API size_t gdr_chunk_workspace_size(const gdr_dims *dims);
 
 /*

@@ -187,17 +187,15 @@ def gdr_chunk_fwd(q, k, v, delta, A, beta, *, delta_bias=None, delta_softplus=Tr
     """Gated delta rule over sequences: q, k (B, L, Hk, K), v (B, L, Hv, V),
     delta, beta (B, L, Hv) bfloat16, A, delta_bias (Hv) float32; returns out
     (B, L, Hv, V).  initial_state and last_state (B, Hv, V, K) float32 may be
-    the same tensor.  scale defaults to K ** -0.5."""
+    the same tensor.  scale defaults to K ** -0.5.  ws is not needed."""
     call = _Call(q, "gdr_chunk_fwd", stream)
     dims, inp, st = _gdr(call, q, k, v, delta, A, beta, delta_bias, delta_softplus, beta_sigmoid, qk_l2norm,
                                scale, False)
     if out is None:
         out = call.like(v)
-    lib = capi()
     f32 = call.f32
-    w, n = call.workspace(lib.gdr_chunk_workspace_size(_ref(dims)), ws)
-    call.run(lib.gdr_chunk_fwd, _ref(dims), _ref(inp), call.ptr(initial_state, "initial_state", st, f32),
-             call.ptr(out, "out", v.shape, call.dtype), call.ptr(last_state, "last_state", st, f32), w, n)
+    call.run(capi().gdr_chunk_fwd, _ref(dims), _ref(inp), call.ptr(initial_state, "initial_state", st, f32),
+             call.ptr(out, "out", v.shape, call.dtype), call.ptr(last_state, "last_state", st, f32), None, 0)
     return out
 
 

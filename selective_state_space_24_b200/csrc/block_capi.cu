@@ -179,15 +179,10 @@ ssm::ResidualArgs residual_args(const norm_dims *d, const residual_norm_params *
 
 extern "C" {
 
-size_t gdr_chunk_workspace_size(const gdr_dims *dims)
-{
-    if (check_gdr_dims(dims, false) != SSM_OK || empty_gdr(dims))
-        return 0;
-    return ssm::gdr_chunk_ws_bytes(gdr_args(dims, nullptr));
-}
+size_t gdr_chunk_workspace_size(const gdr_dims *) { return 0; }
 
 ssm_status gdr_chunk_fwd(const gdr_dims *dims, const gdr_inputs *in, const float *initial_state, void *out,
-                         float *last_state, void *workspace, size_t workspace_bytes, void *stream)
+                         float *last_state, void *, size_t, void *stream)
 {
     ssm_status s = check_gdr_dims(dims, false);
     if (s != SSM_OK)
@@ -203,12 +198,9 @@ ssm_status gdr_chunk_fwd(const gdr_dims *dims, const gdr_inputs *in, const float
     if (!out)
         return SSM_ERR_INVALID_ARG;
     ssm::GdrArgs a = gdr_args(dims, in);
-    if ((s = check_workspace(workspace, workspace_bytes, ssm::gdr_chunk_ws_bytes(a))) != SSM_OK)
-        return s;
     a.init = initial_state;
     a.out = out;
     a.last = last_state;
-    a.workspace = workspace;
     return status(ssm::launch_gdr_chunk(a, st));
 }
 

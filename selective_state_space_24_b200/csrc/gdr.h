@@ -27,7 +27,6 @@ struct GdrArgs {
 // sequences.
 cudaError_t launch_gdr_recurrent(const GdrArgs &a, cudaStream_t st);
 
-size_t gdr_chunk_ws_bytes(const GdrArgs &a);
 cudaError_t launch_gdr_chunk(const GdrArgs &a, cudaStream_t st);
 // Test setting of the chunked forward kernel's bounded waits (process-wide):
 // the chunk to withhold (< 0: none) and the waits' limit (0: the default).

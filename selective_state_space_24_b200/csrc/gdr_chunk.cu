@@ -818,8 +818,6 @@ void gdr_stall_set(int withhold_chunk, unsigned wait_limit)
     g_wait_limit.store(wait_limit);
 }
 
-size_t gdr_chunk_ws_bytes(const GdrArgs &) { return 0; }
-
 namespace {
 
 // Sequences this short go step by step: one chunk takes 16.5 us (K = 128; 11

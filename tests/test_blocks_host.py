@@ -135,6 +135,14 @@ def test_residual_norm_refusals(lib):
     assert lib.residual_norm_bwd_workspace_size(ref(nd(dim=60)), ref(q)) == 0
 
 
+def test_gdr_forward_needs_no_workspace(lib):
+    """Sizes of every kind; so none can be too small or misaligned."""
+    for d in (dims(), dims(L=1), dims(L=100000, K=64), dims(B=300, Hv=96, Hk=1, V=128), dims(B=0), dims(L=0)):
+        assert lib.gdr_chunk_workspace_size(ref(d)) == 0
+    assert fwd(lib, dims(L=0), inputs(q=None), out=None, ws=FAKE + 4, n=3) == OK
+    assert fwd(lib, dims(L=4096), inputs(), out=None) == INVALID   # the first that it finds wrong without one
+
+
 def test_python_refusals():
     """The binding says what is wrong with CPU tensors before any library call."""
     t = torch.zeros(1, 4, 1, 64, dtype=torch.bfloat16)
