@@ -396,3 +396,15 @@ def test_device_timeout_is_reported_and_the_next_call_is_clean(cuda_device, K, c
     assert bool((last == 7.0).all())
     out, again = run_fwd(x, {})
     assert torch.equal(out, want[0]) and torch.equal(again, want[1])
+
+
+@pytest.mark.parametrize("L", [10, 11, 13, 14, 15, 25, 26, 27])
+@pytest.mark.parametrize("heads", [3, 40])
+def test_forward_lengths_around_the_step_by_step_limits(cuda_device, L, heads):
+    """Few and many blocks of state rows, on both sides of where the chunks begin."""
+    for K in (64, 128):
+        x = make(1, L, 1, heads, K, 128, seed=L, init=True)
+        out, last = run_fwd(x, {})
+        ro, rs = ob.gdr(**f64(x))
+        close(out, ro, False)
+        close(last, rs, True)
