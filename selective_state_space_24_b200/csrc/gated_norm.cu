@@ -25,13 +25,6 @@
 namespace ssm {
 namespace {
 
-// Blocks for the rows of one group: as many as rows, at most `most` in all.
-int64_t parts_for(int64_t rows, int64_t groups, const NormPlan &p, int64_t most)
-{
-    const int64_t need = (rows + p.rows_at_once - 1) / p.rows_at_once, share = most / groups;
-    return share < 1 ? 1 : need < share ? need : share;
-}
-
 // GATE: 0 none, 1 before the norm, 2 after it (a variant each: tests of it for
 // every element cost more than the arithmetic they choose).
 template <typename T, int ELEMS, int GATE, bool BWD>
@@ -90,7 +83,7 @@ __global__ void __launch_bounds__(512) gated_norm_kernel(const GatedArgs a, int 
         for (int v = 0; v < NV; v++)
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                sg[v][e] = GATE ? sigmoid_f(zv[v][e]) : 1.f;
+                sg[v][e] = GATE ? sigmoid_mufu(zv[v][e]) : 1.f;
                 const float s = GATE ? zv[v][e] * sg[v][e] : 1.f;
                 const float u = GATE == 1 ? xv[v][e] * s : xv[v][e];
                 sum[0] = fmaf(u, u, sum[0]);
@@ -192,7 +185,7 @@ __global__ void __launch_bounds__(1024) part_sum_kernel(const Sums sums, int dim
         s[threadIdx.y][threadIdx.x] = v;
         __syncthreads();
         // warp y sums column y of the block over the strands
-        const float t = warp_add(s[threadIdx.x][threadIdx.y]);
+        const float t = warp_sum(s[threadIdx.x][threadIdx.y]);
         const int col = blockIdx.x * 32 + threadIdx.y;
         if (threadIdx.x == 0 && col < dim)
             j.out[(size_t)set * dim + col] = t;

@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) prep_kernel(const GdrBwdArgs g, c
                 const float de = gdr_ld(static_cast<const bf16 *>(a.delta), (w.tok + r) * a.Hv + w.h);
                 gl[i] = gdr_log_decay(gdr_dt(de, bias, a.softplus), Ah);
                 const float be = gdr_ld(static_cast<const bf16 *>(a.beta), (w.tok + r) * a.Hv + w.h);
-                s.b[r] = a.sigmoid ? gdr_sigmoid(be) : be;
+                s.b[r] = a.sigmoid ? sigmoid_mufu(be) : be;
             }
         }
         float2 sum[2];
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
         }
         __syncthreads();
         each(xa, m0, nC, [&](int i, int j, float v) { s.x[i * kPX + j] = v; });
-        // Y = -c R' S0 and q = c dO S0, 64 rows of S0 at a time
+        // Y = -c R' S0 and q = c dO S0, 32 rows of S0 at a time
         float Y[2][NK][4], q[2][NK][4];
         zero(Y);
         zero(q);
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kernel(const GdrBwdArgs ga, 
                     const float pre = s.delta[row];
                     // a step that leaves nothing has no gradient, not 0 times an infinite dt either
                     sA = dg[i] != 0.f ? fmaf(dg[i], gdr_dt(pre, bias, a.softplus), sA) : sA;
-                    const float dd = dg[i] * Ah * (a.softplus ? gdr_sigmoid(pre + bias) : 1.f);
+                    const float dd = dg[i] * Ah * (a.softplus ? sigmoid_mufu(pre + bias) : 1.f);
                     sb += dd;
                     gdr_st(static_cast<bf16 *>(ga.ddelta), at, dd);
                     const float db = all(0, row) + all(2, row);

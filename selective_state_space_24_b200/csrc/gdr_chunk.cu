@@ -16,13 +16,16 @@
 // The norms of q and k, b and all decays are scalars of a row or column and
 // stay outside the products: K, Q and V are read as they came.
 //
-// Roundings: K, Q are exact bf16; S, diag(b)(V - ..), T and N enter the
-// products that lead to the state as bf16 pairs hi + lo (at least 16 bits;
-// S K^T and N^T K two products, T .. three), so the state, float32 in
-// registers between chunks, is good to about 2^-17 per product; P, and N and
-// S on the way to the outputs, are single bf16 (out is rounded to bf16
-// anyway).  T is inverted with float32 in its 16 x 16 diagonal blocks and
-// bf16 pairs between them.
+// Roundings: K, Q are exact bf16; S, diag(b)(V - ..), N diag(e), N, T and P
+// enter their products as bf16 pairs hi + lo (at least 16 bits, off by up to
+// 2^-17), two products with K or Q, three (hi hi, hi lo, lo hi) where both
+// factors are pairs.  So the state, float32 in registers between chunks, is
+// 3.8e-6 off the definition in the 2-norm (3.2 to 5.2e-6 over the shapes), where
+// float32 products leave 2e-7: a choice for the chain's length (a third part is
+// half as many products again, and tensor memory is full).  gdr_step is float32
+// throughout, gdr_chunk_bwd's products carry 21 bits.  Outputs are rounded to bf16,
+// 1.7e-3.  T is inverted with float32 in its 16 x 16 diagonal blocks and bf16
+// pairs between them.  Log decays are summed as float pairs (gdr_math.cuh).
 //
 // Per chunk the state's dependence runs S -> S K^T -> (V - ..) -> T .. -> N ->
 // N^T K -> S: three products of the tensor core with a pass of the state's
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c <= nch; c++) {
             const Vec *ve = vec(c);
             const bool more = c < nch;   // else only the last chunk's outputs are left
-            // 1. diag(b)(V - diag(c) K^ S^T), this half's 32 steps
+            // 1. diag(b)(V - diag(c) K^ S^T), this quarter's 16 steps
             if (more && (!wait(&bars.vfull[c & 1], phase2(c)) || !wait(&bars.ready[c & 1], phase2(c)) || !wait(&bars.ks, c & 1)))
                 break;
             fence_after();
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_before();
             arrive1(&bars.n);
-            // 3. S = c_end S + N^T diag(e) K^, this half's columns
+            // 3. S = c_end S + N^T diag(e) K^, this quarter's columns
             if (!wait(&bars.x[half], c & 1))
                 break;
             fence_after();
@@ -716,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 2; e++) {
                 const bool in = c * kC + 2 * lane + e < L;
                 g[e] = in ? gdr_log_decay(gdr_dt(dl[e], bias, a.softplus), Ah) : 0.f;
-                bb[e] = in ? (a.sigmoid ? gdr_sigmoid(be[e]) : be[e]) : 0.f;
+                bb[e] = in ? (a.sigmoid ? sigmoid_mufu(be[e]) : be[e]) : 0.f;
             }
             fetch(c + 1);
             float2 cs[2];

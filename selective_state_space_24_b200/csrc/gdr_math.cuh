@@ -75,15 +75,5 @@ __device__ __forceinline__ float gdr_between(float hi, float lo, float hi0, floa
 {
     return ex2_mufu((hi - hi0) + (lo - lo0));
 }
-// sigmoid(v), also dt's derivative through the softplus
-__device__ __forceinline__ float gdr_sigmoid(float v) { return rcp_mufu(1.f + ex2_mufu(-v * kLog2e)); }
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 
 }  // namespace ssm

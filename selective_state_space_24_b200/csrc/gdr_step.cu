@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdr_recurrent_kernel(const GdrArg
         if (t + 1 < a.L)
             fetch(t + 1, kn, qn, vn, dn, bn);   // the next step's, in flight during this one
         const float dec = ex2_mufu(gdr_dt(dl, bias, a.softplus) * Ah);
-        const float wb = a.sigmoid ? gdr_sigmoid(be) : be;
+        const float wb = a.sigmoid ? sigmoid_mufu(be) : be;
         float kk = 0.f, qq = 0.f, kq = 0.f;
 #pragma unroll
         for (int c = 0; c < C; c++) {

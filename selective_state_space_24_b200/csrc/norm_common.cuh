@@ -111,6 +111,14 @@ template <class Kern> int64_t resident_blocks(Kern kernel, int threads, size_t s
     return (int64_t)kSMs * n;
 }
 
+// Blocks for the rows of one group or set, of which there are `shares`: as many
+// as rows, at most `most` for all of them together.
+inline int64_t parts_for(int64_t rows, int64_t shares, const NormPlan &p, int64_t most)
+{
+    const int64_t need = (rows + p.rows_at_once - 1) / p.rows_at_once, share = most / shares;
+    return share < 1 ? 1 : need < share ? need : share;
+}
+
 // N consecutive float32 (weights next to a vector of N elements)
 template <int N> __device__ __forceinline__ void load_f32(const float *p, float (&f)[N])
 {
@@ -166,16 +174,5 @@ __device__ __forceinline__ float mean_of(float sum, float n, float inv)
     const float q = sum * inv;
     return fmaf(fmaf(-n, q, sum), inv, q);
 }
-
-// the sum over a warp's lanes
-__device__ __forceinline__ float warp_add(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-__device__ __forceinline__ float sigmoid_f(float z) { return rcp_mufu(1.f + ex2_mufu(-z * kLog2e)); }
 
 }  // namespace ssm

@@ -28,13 +28,6 @@
 namespace ssm {
 namespace {
 
-// Blocks for the rows of one set: as many as rows, at most `most` in all.
-int64_t parts_for(int64_t rows, int64_t sets, const NormPlan &p, int64_t most)
-{
-    const int64_t need = (rows / sets + p.rows_at_once - 1) / p.rows_at_once, share = most / sets;
-    return share < 1 ? 1 : need < share ? need : share;
-}
-
 // The sets of rows that never share a block: the samples where a scale's
 // gradient is summed over each of them, else all rows are one.
 int64_t row_sets(int64_t samples, bool has_scale) { return has_scale ? samples : 1; }
@@ -427,7 +420,7 @@ template <typename T, typename R> cudaError_t bwd_typed(const ResidualArgs &a, c
     unsigned blocks = 0;
     auto go = [&](auto elems, auto layer, auto bias, auto scale, auto post) {
         auto kernel = residual_bwd_kernel<T, R, elems.value, layer.value, bias.value, scale.value, post.value>;
-        const int parts = (int)parts_for(a.rows, sets, p, resident_blocks(kernel, p.threads, smem));
+        const int parts = (int)parts_for(a.rows / sets, sets, p, resident_blocks(kernel, p.threads, smem));
         blocks = (unsigned)(sets * parts);
         kernel<<<blocks, p.threads, smem, st>>>(a, p.tpr, p.rows_at_once, parts);
     };
@@ -464,7 +457,7 @@ size_t residual_bwd_workspace(int64_t rows, int64_t samples, int dim, bool has_b
     const int64_t sets = row_sets(samples, has_scale);
     const size_t kinds = 1 + has_bias + has_scale + has_post;
     const NormPlan p = norm_threads(dim);
-    return kinds * (size_t)sets * parts_for(rows, sets, p, (int64_t)kSMs * (2048 / p.threads)) * dim * sizeof(float);
+    return kinds * (size_t)sets * parts_for(rows / sets, sets, p, (int64_t)kSMs * (2048 / p.threads)) * dim * sizeof(float);
 }
 
 cudaError_t launch_residual_fwd(const ResidualArgs &a, cudaStream_t st)

@@ -22,6 +22,17 @@ __device__ __forceinline__ float rcp_mufu(float v)
     return r;
 }
 
+__device__ __forceinline__ float sigmoid_mufu(float v) { return rcp_mufu(1.f + ex2_mufu(-v * kLog2e)); }
+
+// the sum over a warp's lanes
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // softplus(v) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], with
 // log1p(e) = e q(e) and q a degree-7 minimax polynomial for log1p(e) / e on
 // [0, 1] (relative error 3.4e-7 in fp32; coefficients from fit_polys.py).
