@@ -19,7 +19,9 @@
 // sum's round trip per row).  Backward, 16384 rows of 2048: 80 us (4.2 TB/s,
 // 0.64): a row's five operands are unpacked, gated and packed at about 14
 // instructions an element, and the row's sum joins eight warps at a barrier,
-// which four blocks of 256 threads per SM cover in part.
+// which four blocks of 256 threads per SM cover in part.  float32: 61 us forward
+// (1.0 of a copy), 110 backward (0.93).  Rows above 4096 spill (norm_threads):
+// backward, 4096 rows of 8192, bf16 125 us (0.41), float32 185 (0.55).
 #include "norm_common.cuh"
 
 namespace ssm {

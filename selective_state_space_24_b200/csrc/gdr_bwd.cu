@@ -44,14 +44,15 @@
 // per two-part product) and the instructions that feed it: in the chains the
 // tensor pipe is 41% busy and 52% of the issue slots are taken on average, 56%
 // and 70% on the SMs with two blocks; HBM 13%.  Measured on B200, 2 x 2048, 8 key and 16 value heads,
-// K = V = 128: 666 us (preparation 85, the chains 299, the gradients 290, the sum
-// 4); 2 x 197, 6 heads of 64: 58 us, the latency of four launches.  On the way:
+// K = V = 128: 687 us (preparation 89, the chains 313, the gradients 296, the sum
+// 4); 2 x 197, 6 heads of 64: 60 us, the latency of four launches.  On the way:
 // 3780 us with FMA units, 890 with two-part tf32, 756 with the parts taken by
 // integer operations instead of cvt.tf32 (4 clocks against 2), 711 with two
 // preparation blocks per SM, 703 (and 72 -> 59 us) with the chains together: by
 // themselves, with two buffers a tile, they took 135 and 174 us; 666 with V,
 // delta and the second reading of S0 brought in by asynchronous copies ahead of
-// their use in the gradients.  512 threads a block for the gradients were slower
+// their use in the gradients; 669 with the log decays as pairs, 687 with the first
+// parts rounded, which halves what dA is off.  512 threads a block for the gradients were slower
 // (registers), the next head's tiles brought into L2 ahead no faster.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

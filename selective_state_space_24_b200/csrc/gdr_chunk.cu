@@ -40,20 +40,20 @@
 // through tensor memory and the barriers between them, 3.7-3.8 us a chunk,
 // whatever HBM and the tensor cores could do.  So one block of 28 warps per
 // SM, a role each, and nothing but the dependence between two chunks' states.
-// Measured on B200, K = V = 128: 1 x 4096, 32 heads 232 us; 4 x 8192, 32
-// heads (128 blocks for 148 SMs) 540 us after a flush of L2, 482 behind another
-// call, 0.31 of the time of its bytes.  Steps on the way, 4 x 8192: 9650 us on
+// Measured on B200, K = V = 128: 1 x 4096, 32 heads 233 us; 4 x 8192, 32
+// heads (128 blocks for 148 SMs) 541 to 553 us on different GPUs, 0.30 of the
+// rate of a copy.  Steps on the way, 4 x 8192: 9650 us on
 // FMA units, 620 with the chain on the tensor cores, 576 with the outputs
 // behind T's product, 540 with the scalars laid out for packed arithmetic and
 // waits that poll less, then K K^T of the chunk after next issued behind T's
-// product.
+// product.  (Log decays as float pairs cost 0.5 to 1% of these.)
 //
 // The size of the code counts too.  Seven loops run on an SM at once, and
 // where more than about 14 SMs of a GPC run them their instruction cache
 // misses: 3.7 us a chunk with 112 blocks, 4.7 with 148, a third of the warps'
-// stalls "no instruction".  So what appeared twice appears once and products are
+// stalls "no instruction" (before what follows).  So what appeared twice appears once and products are
 // issued from loops over 64 columns: 128 blocks 4.16 -> 3.77 us a chunk, 148
-// 4.70 -> 4.15.  (One code for all rows of T saves another 4 KB, 148 blocks
+// 4.70 -> 4.15 (4.17 now).  (One code for all rows of T saves another 4 KB, 148 blocks
 // 3.80 us, but lengthens T's latency: 128 blocks 3.95; loops of single products
 // issue too slowly: 16 blocks 3.47 -> 3.65.)
 #include <atomic>

@@ -88,7 +88,11 @@ constexpr int kSMs = 148;
 // Threads for rows of `len` elements normed together.  Eight elements a
 // thread (one or two 16-byte words) leave room for several blocks per SM:
 // the norm of 128-channel heads (262144 rows, bf16) took 61 us with sixteen
-// and 40 with eight and the next row's loads ahead, for which they leave room; rows above 4096 need sixteen to stay within 512 threads.
+// and 40 with eight and the next row's loads ahead, for which they leave room.
+// Rows above 4096 need sixteen to stay within 512 threads, which in the
+// gradients (column sums, and the next row) do not fit 128 registers: those
+// variants spill, up to 1.9 KB a thread, and take 1.4 to 3.5 times their bytes'
+// time.
 inline NormPlan norm_threads(int len)
 {
     NormPlan p;
